@@ -239,6 +239,159 @@ int afx_restore_gemm_async(const afx_info *info, const void *blob_dev, uint64_t 
  * x (AFX_E_INVALID_ARG). Errors otherwise as afx_restore_gemm_async. */
 int afx_restore_gemm_batch_async(const afx_gemv_job *jobs, size_t n_jobs, uint32_t m, void *stream);
 
+/* ---- The feed-forward half of a layer around those products, over coded
+ * weights ("Why Weight Offloading Slows Inference", section "Lossless
+ * compression": the bits are reconstructed before the computation that uses
+ * them). A coded weight is a constant: gradients are formed for activations,
+ * and for the norms' own (uncoded) weights and gates. All buffers are device
+ * memory owned by the caller; a workspace holds nothing between calls, and
+ * calls that may run at the same time (two streams, two captured graphs)
+ * each need their own. Strides count elements between rows (tokens). */
+
+typedef enum afx_act {
+    AFX_ACT_SILU = 0,      /* g / (1 + e^-g) */
+    AFX_ACT_GELU_TANH = 1, /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+    AFX_ACT_GELU = 2       /* 0.5 g (1 + erf(g / sqrt(2))) */
+} afx_act;
+
+/* The two projections of a gated feed-forward block: the tensors of two
+ * blobs, both taken as row-major [rows, cols] (rows * cols == n_elems). */
+typedef struct afx_gated {
+    const afx_info *gate_info;  /* filled by afx_query from host copies */
+    const void *gate_blob_dev;  /* device copies of the blobs, 16-byte aligned */
+    const afx_info *up_info;
+    const void *up_blob_dev;
+    uint64_t rows, cols;
+    uint32_t act; /* an afx_act */
+} afx_gated;
+
+/* afx_restore_gated_workspace: bytes of device workspace that
+ * afx_restore_gated_async (backward == 0) or
+ * afx_restore_gated_backward_async (backward != 0) needs for m tokens. Host
+ * only. Errors: AFX_E_INVALID_ARG (NULL, a zero size), AFX_E_UNSUPPORTED
+ * (cols not a multiple of 8, rows >= 2^21, cols >= 2^22, m > 2^23). */
+int afx_restore_gated_workspace(uint64_t rows, uint64_t cols, uint32_t m, int backward, size_t *bytes);
+
+/* afx_restore_gated_async: h = act(x Wg^T) * (x Wu^T) for m tokens, x BF16
+ * [m, cols], h BF16 [m, rows]; any m (0 does nothing), any rows, cols a
+ * multiple of 8. The sums g = x Wg^T and u = x Wu^T, the activation and the
+ * product are FP32; h is rounded to BF16 once. With g_dev and u_dev (both
+ * or neither) g and u are written too, rounded to BF16, for the backward
+ * pass. Results are the same bits on every run. Enqueued on stream; returns
+ * without waiting. No output or workspace may share a byte with an input or
+ * with another output. Errors: as afx_decode_layer_async; AFX_E_INVALID_ARG
+ * (NULL pointer, rows * cols != n_elems, one of g_dev and u_dev, a stride
+ * shorter than its row, unknown act, buffers sharing bytes),
+ * AFX_E_UNSUPPORTED (sizes as above, x_stride not a multiple of 8, a stride
+ * >= 2^22), AFX_E_MISALIGNED (blobs, x or workspace not 16-byte aligned),
+ * AFX_E_BUFFER_TOO_SMALL (workspace). */
+int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_dev, uint64_t x_stride, uint16_t *h_dev,
+                            uint64_t h_stride, uint16_t *g_dev, uint16_t *u_dev, uint64_t gu_stride, void *ws_dev,
+                            size_t ws_bytes, void *stream);
+
+/* afx_restore_gated_backward_async: the gradients of afx_restore_gated_async
+ * for dh FP32 [m, rows] (as afx_restore_gemm_t_async writes it), from the g
+ * and u it kept: dg = dh u act'(g), du = dh act(g), dx = dg Wg + du Wu, dx
+ * BF16 [m, cols]. dg and du are rounded to BF16 (the matrix cores' operand
+ * type) and dx is their FP32 sum, rounded to BF16 once. With dg_dev and
+ * du_dev (both or neither, rows gu_stride apart like g and u) they are
+ * written too: the gradient of a weight matrix, where a program keeps one,
+ * is dg^T x or du^T x. dg_dev may be g_dev and du_dev may be u_dev (in
+ * place); otherwise nothing may overlap. Same bits on every run. Errors: as
+ * afx_restore_gated_async (dh 4-byte aligned). */
+int afx_restore_gated_backward_async(const afx_gated *w, uint32_t m, const float *dh_dev, uint64_t dh_stride,
+                                     const uint16_t *g_dev, const uint16_t *u_dev, uint64_t gu_stride,
+                                     uint16_t *dx_dev, uint64_t dx_stride, uint16_t *dg_dev, uint16_t *du_dev,
+                                     void *ws_dev, size_t ws_bytes, void *stream);
+
+/* afx_restore_gemm_t_workspace: bytes of device workspace that
+ * afx_restore_gemm_t_async needs for m tokens. Host only. Errors:
+ * AFX_E_INVALID_ARG (NULL, a zero size), AFX_E_UNSUPPORTED (rows or cols not
+ * a multiple of 8, rows >= 2^21, cols >= 2^22, m > 2^23). */
+int afx_restore_gemm_t_workspace(uint64_t rows, uint64_t cols, uint32_t m, size_t *bytes);
+
+/* afx_restore_gemm_t_async: y = d W (add == 0) or y += d W (add != 0), where
+ * W is the tensor of the device blob taken as row-major [rows, cols], d is
+ * BF16 [m, rows] and y FP32 [m, cols], both row-major without gaps: the
+ * input gradient of afx_restore_gemm_async's product y = x W^T. Any m (0
+ * does nothing). Sums are FP32, in an order that depends on the sizes only:
+ * the same bits on every run. Enqueued on stream; returns without waiting.
+ * y and the workspace may not share a byte with the blob, d or each other.
+ * Errors: as afx_decode_layer_async; AFX_E_INVALID_ARG (NULL pointer, rows *
+ * cols != n_elems, buffers sharing bytes), AFX_E_UNSUPPORTED (sizes as
+ * above), AFX_E_MISALIGNED (blob, d or workspace not 16-byte aligned, y not
+ * 4-byte aligned), AFX_E_BUFFER_TOO_SMALL (workspace). */
+int afx_restore_gemm_t_async(const afx_info *info, const void *blob_dev, uint64_t rows, uint64_t cols,
+                             const uint16_t *d_dev, uint32_t m, float *y_dev, int add, void *ws_dev, size_t ws_bytes,
+                             void *stream);
+
+#define AFX_MAX_NORM_WIDTH 32768u
+
+typedef enum afx_type { AFX_TYPE_BF16 = 0, AFX_TYPE_FP32 = 1 } afx_type;
+
+/* What stands between two blocks of a layer: a norm after the first, its
+ * gate and residual scale, the residual add, and the norm before the second.
+ *   bh = b * rsqrt(mean(b^2) + eps) * w_post   (w_post NULL: bh = b)
+ *   r' = r + scale * gate * bh                 (gate NULL: 1)
+ *   xn = r' * rsqrt(mean(r'^2) + eps) * w_pre
+ * means over the d values of a row. The residual stream r, r' (and its
+ * gradients) has type r_type; b is FP32 (a product's y), xn BF16 (a
+ * product's x). */
+typedef struct afx_block_norm {
+    uint64_t d;             /* width, 1..AFX_MAX_NORM_WIDTH */
+    float eps;              /* > 0 */
+    float scale;            /* a constant of the block: it has no gradient here */
+    uint32_t r_type;        /* an afx_type */
+    const uint16_t *w_post; /* device, BF16 [d], or NULL */
+    const uint16_t *gate;   /* device, BF16 [d] (gate_stride 0) or [m, d], or NULL */
+    uint64_t gate_stride;   /* 0: one gate for all rows; else elements between rows, >= d */
+    const uint16_t *w_pre;  /* device, BF16 [d], or NULL (no xn) */
+} afx_block_norm;
+
+/* afx_block_norm_async: r' and xn of m rows. b_dev NULL: r' = r (only the
+ * norm before a block; w_post and gate are not read). r_out_dev (r') may be
+ * r_dev itself with the same stride, or NULL when b_dev is NULL; xn_dev may
+ * be NULL exactly when w_pre is. xn is computed from r' before r' is rounded
+ * to r_type. All arithmetic is FP32 and each output is rounded once. Any m
+ * (0 does nothing), any width up to AFX_MAX_NORM_WIDTH; fastest when d and
+ * the strides are multiples of 8 and the buffers 16-byte aligned. Squares
+ * are FP32: a value above about 1e19 overflows its row's mean to infinity.
+ * Enqueued on stream; returns without waiting. Errors: AFX_E_INVALID_ARG
+ * (NULL pointer, d 0, eps not > 0, scale not finite, unknown r_type, a
+ * stride shorter than d, nothing to write, outputs sharing bytes with each
+ * other or an input), AFX_E_UNSUPPORTED (d above AFX_MAX_NORM_WIDTH,
+ * a stride of 2^28 or more), AFX_E_MISALIGNED (a pointer not aligned to its element), AFX_E_HIP. */
+int afx_block_norm_async(const afx_block_norm *p, uint32_t m, const float *b_dev, uint64_t b_stride, const void *r_dev,
+                         uint64_t r_stride, void *r_out_dev, uint64_t r_out_stride, uint16_t *xn_dev,
+                         uint64_t xn_stride, void *stream);
+
+/* afx_block_norm_workspace: bytes of device workspace that
+ * afx_block_norm_backward_async needs for m rows. Host only. Errors:
+ * AFX_E_INVALID_ARG, AFX_E_UNSUPPORTED as above. */
+int afx_block_norm_workspace(const afx_block_norm *p, uint32_t m, size_t *bytes);
+
+/* afx_block_norm_backward_async: the gradients of afx_block_norm_async from
+ * b and r' (r_out, as it was written) and the gradients dxn (BF16) and
+ * dr_out (r_type) of its outputs, either of which may be NULL (zero; dxn
+ * must be NULL when w_pre is):
+ *   dr  = dr_out + the gradient of xn through r'     [m, d] of r_type
+ *   db  = the gradient of r' through b               [m, d] BF16 (a product's d)
+ *   dw_pre = sum over rows of dxn r' rsqrt(..)       FP32 [d]
+ *   dw_post, and dgate: FP32 [d], or dgate FP32 [m, d] when gate_stride != 0
+ * Each output may be NULL (not computed). dr_dev may be dr_out_dev itself
+ * with the same stride. dr is used unrounded in the others. b_dev NULL: only
+ * dr and dw_pre. The sums over rows are FP32 and their order depends on the
+ * sizes only: the same bits on every run; with m == 0 they are written as
+ * zeros. Errors: as afx_block_norm_async (asking for dw_pre without w_pre,
+ * dw_post without w_post, dgate without gate, or db, dw_post or dgate
+ * without b is AFX_E_INVALID_ARG); AFX_E_BUFFER_TOO_SMALL (workspace),
+ * AFX_E_MISALIGNED also for a workspace not 16-byte aligned. */
+int afx_block_norm_backward_async(const afx_block_norm *p, uint32_t m, const float *b_dev, uint64_t b_stride,
+                                  const void *r_out_dev, uint64_t r_out_stride, const uint16_t *dxn_dev,
+                                  uint64_t dxn_stride, const void *dr_out_dev, uint64_t dr_out_stride, void *dr_dev,
+                                  uint64_t dr_stride, uint16_t *db_dev, uint64_t db_stride, float *dw_pre_dev,
+                                  float *dw_post_dev, float *dgate_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
 /* ---- Unpack on the host. "Why Weight Offloading Slows Inference" (section
  * "The path from storage to the GPU", Figure 1) unpacks a compressed weight
  * in RAM between the read and the copy to the GPU, and section "Lossless

@@ -26,13 +26,19 @@ AFX_E_IO = -9
 AFX_E_HOST_MEMORY = -10
 MAX_JOBS_PER_LAUNCH = 32
 AFX_READ_DIRECT = 1
+ACT_SILU, ACT_GELU_TANH, ACT_GELU = 0, 1, 2
+TYPE_BF16, TYPE_FP32 = 0, 1
+MAX_NORM_WIDTH = 32768
 
 # Every symbol include/afx.h declares.
 EXPORTS = ("afx_query", "afx_decode_tensor", "afx_decode_layer_async", "afx_decode_layer_grid_async",
            "afx_status_str",
            "afx_encode_plan", "afx_encode", "afx_file_read", "afx_decode_host",
            "afx_restore_gemv_async", "afx_restore_gemv_batch_async", "afx_restore_gemm_async",
-           "afx_restore_gemm_batch_async")
+           "afx_restore_gemm_batch_async",
+           "afx_restore_gated_workspace", "afx_restore_gated_async", "afx_restore_gated_backward_async",
+           "afx_restore_gemm_t_workspace", "afx_restore_gemm_t_async",
+           "afx_block_norm_async", "afx_block_norm_workspace", "afx_block_norm_backward_async")
 
 
 class AfxError(RuntimeError):
@@ -87,6 +93,31 @@ class afx_job(ctypes.Structure):
     ]
 
 
+class afx_gated(ctypes.Structure):
+    _fields_ = [
+        ("gate_info", ctypes.POINTER(afx_info)),
+        ("gate_blob_dev", ctypes.c_void_p),
+        ("up_info", ctypes.POINTER(afx_info)),
+        ("up_blob_dev", ctypes.c_void_p),
+        ("rows", ctypes.c_uint64),
+        ("cols", ctypes.c_uint64),
+        ("act", ctypes.c_uint32),
+    ]
+
+
+class afx_block_norm(ctypes.Structure):
+    _fields_ = [
+        ("d", ctypes.c_uint64),
+        ("eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("r_type", ctypes.c_uint32),
+        ("w_post", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("gate_stride", ctypes.c_uint64),
+        ("w_pre", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -133,6 +164,23 @@ def lib() -> ctypes.CDLL:
         L.afx_restore_gemm_async.restype = ctypes.c_int
         L.afx_restore_gemm_batch_async.argtypes = L.afx_restore_gemv_batch_async.argtypes
         L.afx_restore_gemm_batch_async.restype = ctypes.c_int
+        ptr, u32, u64, size = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t
+        sizep, gatedp, normp = ctypes.POINTER(size), ctypes.POINTER(afx_gated), ctypes.POINTER(afx_block_norm)
+        for name, args in (
+                ("afx_restore_gated_workspace", [u64, u64, u32, ctypes.c_int, sizep]),
+                ("afx_restore_gated_async", [gatedp, u32, ptr, u64, ptr, u64, ptr, ptr, u64, ptr, size, ptr]),
+                ("afx_restore_gated_backward_async",
+                 [gatedp, u32, ptr, u64, ptr, ptr, u64, ptr, u64, ptr, ptr, ptr, size, ptr]),
+                ("afx_restore_gemm_t_workspace", [u64, u64, u32, sizep]),
+                ("afx_restore_gemm_t_async",
+                 [ctypes.POINTER(afx_info), ptr, u64, u64, ptr, u32, ptr, ctypes.c_int, ptr, size, ptr]),
+                ("afx_block_norm_async", [normp, u32, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr]),
+                ("afx_block_norm_workspace", [normp, u32, sizep]),
+                ("afx_block_norm_backward_async",
+                 [normp, u32, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, ptr, ptr, ptr, size,
+                  ptr])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -299,7 +347,100 @@ def afx_restore_gemm_batch_async(jobs, m: int, stream: int = 0) -> None:
     make_gemv_jobs, or tuples)."""
     arr = jobs if isinstance(jobs, ctypes.Array) else make_gemv_jobs(jobs)
     _check(lib().afx_restore_gemm_batch_async(arr, len(arr), m, ctypes.c_void_p(stream)),
-           "afx_restore_gemm_batch_async")
+           "afx_restore_gemm_batch_async",
+           "afx_restore_gated_workspace", "afx_restore_gated_async", "afx_restore_gated_backward_async",
+           "afx_restore_gemm_t_workspace", "afx_restore_gemm_t_async",
+           "afx_block_norm_async", "afx_block_norm_workspace", "afx_block_norm_backward_async")
+
+
+def _u32(v: int, what: str) -> int:
+    """A count the C side takes as 32 bits (ctypes would wrap it silently)."""
+    if not 0 <= int(v) < 2 ** 32:
+        raise ValueError(f"{what} {v} is not a 32-bit unsigned count")
+    return int(v)
+
+
+def gated_weights(gate_info: afx_info, gate_blob_dev: int, up_info: afx_info, up_blob_dev: int, rows: int, cols: int,
+                  act: int = ACT_SILU) -> afx_gated:
+    """The two projections of a gated feed-forward block (it refers to the
+    afx_info objects: keep them)."""
+    return afx_gated(ctypes.pointer(gate_info), gate_blob_dev, ctypes.pointer(up_info), up_blob_dev, rows, cols, act)
+
+
+def afx_restore_gated_workspace(rows: int, cols: int, m: int, backward: bool = False) -> int:
+    """Bytes of device workspace of a gated block's forward or backward call."""
+    n = ctypes.c_size_t()
+    _check(lib().afx_restore_gated_workspace(rows, cols, _u32(m, "m"), int(backward), ctypes.byref(n)),
+           "afx_restore_gated_workspace")
+    return n.value
+
+
+def afx_restore_gated_async(w: afx_gated, m: int, x_dev: int, x_stride: int, h_dev: int, h_stride: int, g_dev: int,
+                            u_dev: int, gu_stride: int, ws_dev: int, ws_bytes: int, stream: int = 0) -> None:
+    """h = act(x Wg^T) * (x Wu^T) over coded weights (see afx.h); g_dev and
+    u_dev are 0 when the pre-activations are not kept."""
+    _check(lib().afx_restore_gated_async(ctypes.byref(w), _u32(m, "m"), x_dev, x_stride, h_dev, h_stride, g_dev, u_dev,
+                                         gu_stride, ws_dev, ws_bytes, stream), "afx_restore_gated_async")
+
+
+def afx_restore_gated_backward_async(w: afx_gated, m: int, dh_dev: int, dh_stride: int, g_dev: int, u_dev: int,
+                                     gu_stride: int, dx_dev: int, dx_stride: int, dg_dev: int, du_dev: int,
+                                     ws_dev: int, ws_bytes: int, stream: int = 0) -> None:
+    """dx, and dg and du when their addresses are not 0, from dh and the kept
+    g and u (see afx.h)."""
+    _check(lib().afx_restore_gated_backward_async(ctypes.byref(w), _u32(m, "m"), dh_dev, dh_stride, g_dev, u_dev,
+                                                  gu_stride, dx_dev, dx_stride, dg_dev, du_dev, ws_dev, ws_bytes,
+                                                  stream), "afx_restore_gated_backward_async")
+
+
+def afx_restore_gemm_t_workspace(rows: int, cols: int, m: int) -> int:
+    """Bytes of device workspace of afx_restore_gemm_t_async."""
+    n = ctypes.c_size_t()
+    _check(lib().afx_restore_gemm_t_workspace(rows, cols, _u32(m, "m"), ctypes.byref(n)),
+           "afx_restore_gemm_t_workspace")
+    return n.value
+
+
+def afx_restore_gemm_t_async(info: afx_info, blob_dev: int, rows: int, cols: int, d_dev: int, m: int, y_dev: int,
+                             add: bool, ws_dev: int, ws_bytes: int, stream: int = 0) -> None:
+    """y = d W, or y += d W with add: the input gradient of the product with
+    a coded matrix (see afx.h)."""
+    _check(lib().afx_restore_gemm_t_async(ctypes.byref(info), blob_dev, rows, cols, d_dev, _u32(m, "m"), y_dev,
+                                          int(add), ws_dev, ws_bytes, stream), "afx_restore_gemm_t_async")
+
+
+def block_norm(d: int, eps: float, scale: float = 1.0, r_type: int = TYPE_BF16, w_post: int = 0, gate: int = 0,
+               gate_stride: int = 0, w_pre: int = 0) -> afx_block_norm:
+    """What stands between two blocks: device addresses of the weights and
+    the gate, 0 for those it does without."""
+    return afx_block_norm(d, eps, scale, r_type, w_post, gate, gate_stride, w_pre)
+
+
+def afx_block_norm_async(p: afx_block_norm, m: int, b_dev: int, b_stride: int, r_dev: int, r_stride: int,
+                         r_out_dev: int, r_out_stride: int, xn_dev: int, xn_stride: int, stream: int = 0) -> None:
+    """r' = r + scale gate norm(b; w_post) and xn = norm(r'; w_pre) (see afx.h)."""
+    _check(lib().afx_block_norm_async(ctypes.byref(p), _u32(m, "m"), b_dev, b_stride, r_dev, r_stride, r_out_dev,
+                                      r_out_stride, xn_dev, xn_stride, stream), "afx_block_norm_async")
+
+
+def afx_block_norm_workspace(p: afx_block_norm, m: int) -> int:
+    """Bytes of device workspace of afx_block_norm_backward_async."""
+    n = ctypes.c_size_t()
+    _check(lib().afx_block_norm_workspace(ctypes.byref(p), _u32(m, "m"), ctypes.byref(n)), "afx_block_norm_workspace")
+    return n.value
+
+
+def afx_block_norm_backward_async(p: afx_block_norm, m: int, b_dev: int, b_stride: int, r_out_dev: int,
+                                  r_out_stride: int, dxn_dev: int, dxn_stride: int, dr_out_dev: int,
+                                  dr_out_stride: int, dr_dev: int, dr_stride: int, db_dev: int, db_stride: int,
+                                  dw_pre_dev: int, dw_post_dev: int, dgate_dev: int, ws_dev: int, ws_bytes: int,
+                                  stream: int = 0) -> None:
+    """The gradients of afx_block_norm_async; an address of 0 leaves an
+    input's gradient out, or an output uncomputed (see afx.h)."""
+    _check(lib().afx_block_norm_backward_async(ctypes.byref(p), _u32(m, "m"), b_dev, b_stride, r_out_dev, r_out_stride,
+                                               dxn_dev, dxn_stride, dr_out_dev, dr_out_stride, dr_dev, dr_stride,
+                                               db_dev, db_stride, dw_pre_dev, dw_post_dev, dgate_dev, ws_dev, ws_bytes,
+                                               stream), "afx_block_norm_backward_async")
 
 
 def afx_decode_host(blob, blob_bytes: int | None = None, out=None, threads: int = 0):

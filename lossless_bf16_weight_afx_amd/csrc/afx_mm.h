@@ -1,0 +1,51 @@
+// afx_mm.h -- the product of BF16 activations with restored BF16 weights on
+// the matrix cores (afx_mm.hip), as the gated feed-forward block and the
+// transposed product use it. Not installed.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "afx_internal.h"
+
+namespace afx {
+
+// Columns of a k-tile, and the multiple to which the reduction of a two-matrix
+// product is padded (so that no k-tile crosses from one matrix to the next).
+constexpr uint32_t kMmTileK = 64;
+constexpr uint64_t mm_pad_k(uint64_t k) { return (k + kMmTileK - 1) / kMmTileK * kMmTileK; }
+
+// The activation of a gated block (afx_act), as compile-time choice.
+struct MmGated {
+    const uint16_t *x;       // BF16 [m, cols], row stride ldx
+    uint64_t ldx;
+    uint32_t m;
+    const uint16_t *wg, *wu; // BF16 [rows, cols], restored
+    uint64_t rows, cols;
+    uint32_t act;
+    uint16_t *h;             // BF16 [m, rows], row stride ldh
+    uint64_t ldh;
+    uint16_t *g, *u;         // BF16 [m, rows], row stride ldgu, or NULL
+    uint64_t ldgu;
+};
+
+// y = sum over the matrices i of a[:, i kpad .. i kpad + rows) w_i, with
+// kpad = mm_pad_k(rows) when n_mats is 2.
+struct MmTransposed {
+    const uint16_t *a;       // BF16 [m, n_mats kpad] (one matrix: [m, rows]), row stride lda
+    uint64_t lda;
+    uint32_t m;
+    const uint16_t *w[2];    // BF16 [rows, cols], restored
+    uint32_t n_mats;
+    uint64_t rows, cols;
+    float *y32;              // FP32 [m, cols], row stride ldy (one of y32, y16)
+    uint16_t *y16;           // BF16
+    uint64_t ldy;
+    bool add;                // y32 += instead of =
+    float *partial;          // mm_transposed_partial(...) bytes
+};
+
+uint64_t mm_transposed_partial(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m);
+int launch_mm_gated(const MmGated &p, hipStream_t stream);
+int launch_mm_transposed(const MmTransposed &p, hipStream_t stream);
+
+}  // namespace afx
