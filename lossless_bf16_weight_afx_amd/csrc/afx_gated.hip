@@ -16,6 +16,7 @@
 #include <cstring>
 
 #include "afx_act.h"
+#include "afx_gated_gemv.h"
 #include "afx_mm.h"
 
 namespace afx {
@@ -152,6 +153,10 @@ struct GatedSpace {
 GatedSpace gated_space(uint64_t rows, uint64_t cols, uint32_t m, bool backward) {
     GatedSpace s{};
     if (m == 0) return s;
+    if (!backward && m <= kGatedGemvTokens) {
+        s.bytes = gated_gemv_space(rows, cols, m);
+        return s;
+    }
     const uint64_t w = align_up(2 * rows * cols);
     s.wu = w;
     s.dgu = 2 * w;
@@ -215,6 +220,8 @@ int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_de
     if (any_overlap(in, 3, out, 4) || pairs_overlap(out, 4)) return AFX_E_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(ws_dev);
+    if (m <= kGatedGemvTokens)
+        return launch_gated_gemv(*w, {x_dev, x_stride, m, h_dev, g_dev, u_dev, h_stride, g_dev ? gu_stride : 0}, ws, s);
     rc = restore_pair(w, ws + sp.wg, ws + sp.wu, s);
     if (rc != AFX_OK) return rc;
     MmGated p{};
