@@ -16,6 +16,7 @@
 #include <cstring>
 
 #include "afx_act.h"
+#include "afx_gated_gemm.h"
 #include "afx_gated_gemv.h"
 #include "afx_mm.h"
 
@@ -146,6 +147,16 @@ int check_sizes(uint64_t rows, uint64_t cols, uint32_t m) {
     return cols % 8 || rows >= kMaxRows || cols >= kMaxCols || m > kMaxTokens ? AFX_E_UNSUPPORTED : AFX_OK;
 }
 
+// Which kernels run a forward call. One to four tokens: the matrix-vector
+// kernel. Up to 128: the fused matrix-core kernel, if rows hold whole groups
+// of the coded format. Else the matrices are restored to the workspace and
+// multiplied there.
+enum GatedPath { kPathGemv, kPathGemm, kPathRestore };
+GatedPath gated_path(uint64_t cols, uint32_t m) {
+    if (m <= kGatedGemvTokens) return kPathGemv;
+    return m <= kGatedGemmTokens && cols % kGroup == 0 ? kPathGemm : kPathRestore;
+}
+
 // Where the pieces of a gated call's workspace lie, and its size.
 struct GatedSpace {
     uint64_t wg, wu, dgu, partial, bytes;
@@ -153,8 +164,9 @@ struct GatedSpace {
 GatedSpace gated_space(uint64_t rows, uint64_t cols, uint32_t m, bool backward) {
     GatedSpace s{};
     if (m == 0) return s;
-    if (!backward && m <= kGatedGemvTokens) {
-        s.bytes = gated_gemv_space(rows, cols, m);
+    const GatedPath path = gated_path(cols, m);
+    if (!backward && path != kPathRestore) {
+        s.bytes = path == kPathGemv ? gated_gemv_space(rows, cols, m) : gated_gemm_space(rows, cols, m);
         return s;
     }
     const uint64_t w = align_up(2 * rows * cols);
@@ -220,8 +232,10 @@ int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_de
     if (any_overlap(in, 3, out, 4) || pairs_overlap(out, 4)) return AFX_E_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(ws_dev);
-    if (m <= kGatedGemvTokens)
-        return launch_gated_gemv(*w, {x_dev, x_stride, m, h_dev, g_dev, u_dev, h_stride, g_dev ? gu_stride : 0}, ws, s);
+    const uint64_t gus = g_dev ? gu_stride : 0;
+    const GatedPath path = gated_path(w->cols, m);
+    if (path == kPathGemv) return launch_gated_gemv(*w, {x_dev, x_stride, m, h_dev, g_dev, u_dev, h_stride, gus}, ws, s);
+    if (path == kPathGemm) return launch_gated_gemm(*w, {x_dev, x_stride, m, h_dev, g_dev, u_dev, h_stride, gus}, ws, s);
     rc = restore_pair(w, ws + sp.wg, ws + sp.wu, s);
     if (rc != AFX_OK) return rc;
     MmGated p{};
@@ -237,7 +251,7 @@ int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_de
     p.ldh = h_stride;
     p.g = g_dev;
     p.u = u_dev;
-    p.ldgu = g_dev ? gu_stride : 0;
+    p.ldgu = gus;
     return launch_mm_gated(p, s);
 }
 
