@@ -347,10 +347,7 @@ def afx_restore_gemm_batch_async(jobs, m: int, stream: int = 0) -> None:
     make_gemv_jobs, or tuples)."""
     arr = jobs if isinstance(jobs, ctypes.Array) else make_gemv_jobs(jobs)
     _check(lib().afx_restore_gemm_batch_async(arr, len(arr), m, ctypes.c_void_p(stream)),
-           "afx_restore_gemm_batch_async",
-           "afx_restore_gated_workspace", "afx_restore_gated_async", "afx_restore_gated_backward_async",
-           "afx_restore_gemm_t_workspace", "afx_restore_gemm_t_async",
-           "afx_block_norm_async", "afx_block_norm_workspace", "afx_block_norm_backward_async")
+           "afx_restore_gemm_batch_async")
 
 
 def _u32(v: int, what: str) -> int:
