@@ -19,10 +19,22 @@ struct GatedGemm {
     uint64_t ldh, ldgu;
 };
 
-// Three workgroups on each of 256 CUs run at once. (On a device with fewer
-// CUs the rest follow; the split, and so the workspace and the order of the
-// sums, do not depend on the device.)
-inline GatedSplit gated_split(uint64_t rows, uint64_t cols) { return split_slabs(rows, cols, 3 * 256); }
+// Token blocks of 16 that a call for m tokens computes (a kernel each for 1 to
+// 4, 6 and 8).
+constexpr uint32_t kGatedTokenBlock = 16;
+constexpr uint32_t gated_token_blocks(uint32_t m) {
+    const uint32_t b = (m + kGatedTokenBlock - 1) / kGatedTokenBlock;
+    return b <= 4 ? b : (b + 1) / 2 * 2;
+}
+
+// Waves of a workgroup. One workgroup of each matrix on each of 128 CUs: both
+// matrices fill 256. (On a device with fewer CUs the rest follow; the split,
+// and so the workspace and the order of the sums, do not depend on the
+// device.)
+constexpr uint32_t gated_waves(uint32_t blocks) { return blocks <= 4 ? 16 : 8; }
+inline GatedSplit gated_split(uint64_t rows, uint64_t cols, uint32_t m) {
+    return split_slabs(rows, cols, 128, gated_waves(gated_token_blocks(m)));
+}
 
 // cols: a multiple of 32 (a row of whole groups).
 uint64_t gated_gemm_space(uint64_t rows, uint64_t cols, uint32_t m);

@@ -1,23 +1,29 @@
 // afx_gated_gemm.hip -- the gated block for up to 128 tokens (gfx950): both
-// projections restored slab by slab into LDS and multiplied there on the
-// matrix cores, then the activation and the product. No restored weight
-// reaches memory.
+// projections restored and multiplied on the matrix cores, then the
+// activation and the product. No restored weight reaches memory, or LDS.
 //
-// The restore and the multiplication of a slab (64 weight rows by 256
-// columns) are those of afx_gemm.hip. Here a tile is 32 rows of the gate
-// matrix (restored by waves 0 and 1, with its decode table) and the same 32
-// rows of the up matrix (waves 2 and 3), so that a wave's two accumulators
-// are g and u of the same outputs.
+// A slab is 16 weight rows by 256 columns: 128 groups of 32 values, which
+// decode on their own, two per lane. Lane l takes row l mod 16 and the
+// groups q = l / 16 and q + 4 of it; the 32 values of a group, 8 at a time,
+// are then just what lane l feeds v_mfma_f32_16x16x32_bf16 for row l mod 16,
+// if its four lanes per row may take any 32 columns between them, and they
+// may: the order of a sum's terms is free as long as the tokens' operand has
+// the same. So x is first copied into that order, each operand's 1 KB in one
+// piece (x's own rows, 2 cols bytes apart, would fall into a few sets of the
+// L1).
 //
-// Decoding bounds this, so the work is split evenly: the slabs of all tiles,
-// in order, are cut into one contiguous range per resident workgroup, whose
-// loads run ahead across the ends of tiles. A range's sums for a tile go to
-// the workspace in FP32, and a second launch adds a tile's ranges in order
-// and forms h: the same bits on every run.
+// The decode's instructions and the coded bytes bound this, so the waves are
+// independent of each other: every wave stages its own rows' code words,
+// reads the workgroup's pair table, and shares no barrier after that is
+// built. They do go through the same columns at about the same time, so that
+// the CU's L1 serves most of their tokens' operands. The slabs of all tiles
+// (16 rows per wave), in order, are cut into one contiguous range per
+// workgroup; a range's sums for a tile go to the workspace in FP32, and a
+// last launch adds a tile's ranges in order and forms h: the same bits on
+// every run.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "afx_act.h"
 #include "afx_gated_gemm.h"
@@ -26,250 +32,336 @@
 namespace afx {
 namespace {
 
-constexpr int kWaves = 4, kSlabThreads = kWaves * kWave;
-constexpr uint32_t kSlabStride = kSlabCols * 2 + 16;  // bytes per restored row in LDS
-static_assert(kSegRow * 4 <= kSlabStride, "a row's staged words fit its slab row");
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kTok = kGatedTokenBlock;
+constexpr uint32_t kSlabSteps = kSlabCols / 32;  // matrix instructions per slab and token block
 static_assert(kSegWords * 32 >= kSlabCols * kMaxLen + 5 * 32, "a segment's words fit its slice");
 
 struct SlabArgs {
     TensorDesc w[2];     // gate, up
-    const uint16_t *x;   // BF16 [m, cols], row stride ldx
-    float *part;         // [tiles][most ranges of a tile][m][64]
-    uint64_t ldx;
-    uint32_t m, rows, cols;
+    const uint16_t *xp;  // x in operand order: [slab][step][token block][lane][8]
+    float *part[2];      // [part_places][token blocks][16 tokens][16 rows]
+    uint32_t m, rows, cols, blocks;  // blocks: token blocks
     GatedSplit split;
 };
 
-// Bit offsets of the lane's two groups of a row segment and of the segment's
-// end, kept as loaded and added up only where used.
-struct Bits {
-    uint64_t b1, b2, be;
-    uint32_t g1, g2, ge;
-    bool last;  // the segment ends the tensor
+// Operand step (half, j) of a slab: lane l holds columns 128 half + 32 (l /
+// 16) + 8 j .. + 7 of token l mod 16.
+__global__ __launch_bounds__(256) void afx_gated_pack_kernel(const uint16_t *x, uint64_t ldx, uint32_t m,
+                                                             uint32_t cols, uint32_t blocks, uint16_t *out) {
+    // one wave per operand; operand o of (slab, step, token block)
+    const uint32_t o = blockIdx.x * 4 + threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const uint32_t tb = o % blocks, step = o / blocks % kSlabSteps, slab = o / blocks / kSlabSteps;
+    const uint32_t col = slab * kSlabCols + 128 * (step / 4) + 32 * (lane / 16) + 8 * (step % 4);
+    const uint32_t t = tb * kTok + lane % 16;
+    if (slab * kSlabCols >= cols) return;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (t < m && col < cols) v = *reinterpret_cast<const uint4 *>(x + t * ldx + col);
+    *reinterpret_cast<uint4 *>(out + ((uint64_t)o * kWave + lane) * 8) = v;
+}
+
+// A tile's place in its tensor: bases of its first element, so that a lane's
+// own offsets stay 32-bit.
+struct Tile {
+    const uint64_t *base;   // chunk_base of the tile's first chunk
+    const uint16_t *gap;    // gap of its first group
+    const uint8_t *sm;      // its first sign/mantissa byte
+    uint32_t in_chunk;      // its first element's place in that chunk
+    uint32_t left;          // elements from its first to the tensor's end (at most 2^31)
+    uint32_t chunks;        // chunk_base entries from `base` to the last one
 };
-struct Data {  // a segment's first 32 staged words and the lane's sign/mantissa bytes
-    uint64_t wa;
-    uint32_t nw;
-    uint4 w0, w1;
-    u32x4 s1a, s1b, s2a, s2b;
-};
-// Where the lane's groups of a slab (columns k0.. of a tile) lie: its groups
-// start at elements e1, e2, its row's elements of the slab end at e_end. A
-// row past the matrix repeats its last one and a group past a row's end
-// repeats the row's last one: they are decoded, not used.
+__device__ inline Tile tile_at(const TensorDesc &T, uint32_t tile, uint32_t cols) {
+    const uint64_t e0 = (uint64_t)tile * kGatedWaveRows * cols;
+    return Tile{T.chunk_base + (e0 >> 12), T.gap + (e0 >> 5), T.signmant + e0, (uint32_t)e0 & (kChunk - 1),
+                (uint32_t)umin64(T.n - e0, 1u << 31), T.n_chunks - (uint32_t)(e0 >> 12)};
+}
+
+// Loads are in quads of lanes per row (lane l: row l / 4, part c = l mod 4),
+// so that a quad's accesses fall into one cache line; decoding and multiplying
+// are with row l mod 16 and q = l / 16. What the two orders hand over goes
+// through LDS.
+
+// A row's part of a slab: its elements [start, start + len), from the tile's
+// first element.
 struct Seg {
-    uint64_t e1, e2, e_end;
+    uint32_t start, len;
 };
-__device__ inline Seg segment(const SlabArgs &p, uint32_t tile, uint32_t k0, uint32_t row, uint32_t q4) {
-    const uint64_t row_e = (uint64_t)min(tile * kGatedTileRows + row, p.rows - 1) * p.cols;
-    const uint32_t last = p.cols - kGroup;
-    return Seg{row_e + min(k0 + kGroup * q4, last), row_e + min(k0 + kGroup * (q4 + 4), last),
-               row_e + min(k0 + kSlabCols, p.cols)};
-}
-// The slab after (tile, k0).
-__device__ inline void next_slab(const SlabArgs &p, uint32_t &tile, uint32_t &k0) {
-    k0 += kSlabCols;
-    if (k0 >= p.cols) {
-        k0 = 0;
-        ++tile;
-    }
-}
-__device__ inline Bits seg_bits(const TensorDesc &T, const Seg &g) {
+
+// What the bit offsets of the lane's groups 2 c and 2 c + 1 of a segment and
+// of its end are made of, kept as loaded and added up only where used. (A
+// segment lies in one chunk or ends in the next; a group past the row's end
+// repeats the row's last one: it is decoded, not used.)
+struct Bits {
+    u32x4 base;      // u64 bit bases of the chunk that the segment starts in, and of the next
+    uint32_t a, b, e;  // gaps of the lane's groups and of the group after the segment
+    uint32_t next_a, next_b, next_e;  // whether each is in the next chunk
+    uint32_t e_mask;   // 0 where the segment ends the tensor (the stream's end, with no gap)
+};
+__device__ inline Bits seg_bits(const Tile &t, const Seg &g, uint32_t c) {
     Bits b;
-    b.last = g.e_end >= T.n;
-    b.b1 = T.chunk_base[g.e1 >> 12];
-    b.g1 = T.gap[g.e1 >> 5];
-    b.b2 = T.chunk_base[g.e2 >> 12];
-    b.g2 = T.gap[g.e2 >> 5];
-    b.be = T.chunk_base[b.last ? T.n_chunks : g.e_end >> 12];
-    b.ge = T.gap[b.last ? 0 : g.e_end >> 5];
+    const uint32_t ch = (t.in_chunk + g.start) >> 12, most = g.len / kGroup - 1, end = g.start + g.len;
+    const uint32_t ga = min(2 * c, most), gb = min(2 * c + 1, most);
+    __builtin_memcpy(&b.base, t.base + ch, 16);  // (8-byte aligned; the entry after the last chunk's exists)
+    const bool last = end >= t.left;
+    b.a = t.gap[(g.start >> 5) + ga];
+    b.b = t.gap[(g.start >> 5) + gb];
+    b.e = t.gap[last ? 0 : end >> 5];
+    b.next_a = (t.in_chunk + g.start + kGroup * ga) >> 12 != ch;
+    b.next_b = (t.in_chunk + g.start + kGroup * gb) >> 12 != ch;
+    b.next_e = last || (t.in_chunk + end) >> 12 != ch;
+    b.e_mask = last ? 0u : ~0u;
     return b;
 }
-__device__ inline uint64_t bit1(const Bits &b) { return b.b1 + b.g1; }
-__device__ inline uint64_t bit2(const Bits &b) { return b.b2 + b.g2; }
-__device__ inline uint64_t bit_end(const Bits &b) { return b.be + (b.last ? 0u : b.ge); }
-__device__ inline Data seg_data(const TensorDesc &T, const Seg &g, uint32_t q4, const Bits &b) {
-    Data d;
-    const uint64_t p_lo = quad_first(bit1(b)), p_hi = bit_end(b);
-    d.wa = seg_first_word(p_lo);
-    d.nw = seg_words(p_lo, p_hi);
-    d.w0 = load_words4(T, d.wa + 4 * q4);
-    d.w1 = load_words4(T, d.wa + 16 + 4 * q4);
-    const u32x4 *sm1 = reinterpret_cast<const u32x4 *>(T.signmant + g.e1);
-    const u32x4 *sm2 = reinterpret_cast<const u32x4 *>(T.signmant + g.e2);
-    d.s1a = __builtin_nontemporal_load(sm1);
-    d.s1b = __builtin_nontemporal_load(sm1 + 1);
-    d.s2a = __builtin_nontemporal_load(sm2);
-    d.s2b = __builtin_nontemporal_load(sm2 + 1);
-    return d;
+
+// A row segment's staged words [wa, wa + nw), and where the lane's groups
+// start in them, in bits (16 each). Differences of positions are taken modulo
+// 2^32: they are small, or, on a corrupt stream, clamped.
+struct Words {
+    uint64_t wa;
+    uint32_t nw, starts;
+};
+__device__ inline Words seg_words_of(const Bits &b) {
+    const uint64_t b0 = ((uint64_t)b.base.y << 32) | b.base.x, bn = ((uint64_t)b.base.w << 32) | b.base.z;
+    const uint64_t pa = (b.next_a ? bn : b0) + b.a;
+    Words w;
+    w.wa = seg_first_word(quad_first(pa));
+    const uint32_t first = (uint32_t)w.wa << 5;
+    w.nw = min((((b.next_e ? b.base.z : b.base.x) + (b.e & b.e_mask) - first + 31) >> 5) + 1, kSegWords);
+    w.starts = min((uint32_t)pa - first, kSegMaxStart) |
+               min((b.next_b ? b.base.z : b.base.x) + b.b - first, kSegMaxStart) << 16;
+    return w;
+}
+static_assert(kSegMaxStart < 1u << 16, "a start fits 16 bits");
+
+// The counters of the chains of the lane's groups q and q + 4 of row l mod 16.
+__device__ inline void chain_starts(uint32_t starts, uint32_t lane, uint32_t &r1, uint32_t &r2) {
+    const int at = (int)(16 * (lane & 15) + 4 * (lane >> 5));  // lane 4 row + q / 2
+    const uint32_t v1 = (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)starts);
+    const uint32_t v2 = (uint32_t)__builtin_amdgcn_ds_bpermute(at + 8, (int)starts);
+    const uint32_t shift = lane & 16;  // q odd: the high half
+    r1 = 32 * kSegRev + kLead - ((v1 >> shift) & 0xFFFF);
+    r2 = 32 * kSegRev + kLead - ((v2 >> shift) & 0xFFFF);
 }
 
+// The 32 exponent codes of the lane's two groups through the pair table (the
+// chains start kLead bits early, so the pad word above the staged words may
+// be read, never used).
+__device__ inline void decode_pairs(const uint32_t *seg, uint32_t r1, uint32_t r2, const uint32_t *plut,
+                                    uint32_t (&ex1)[8], uint32_t (&ex2)[8]) {
+    BufChain A = buf_chain(seg, r1), B = buf_chain(seg, r2);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        uint32_t a01, b01, a23, b23;
+        pair_chain_steps(A, B, seg, plut, a01, b01);
+        pair_chain_steps(A, B, seg, plut, a23, b23);
+        ex1[q] = join_entries(a01, a23);
+        ex2[q] = join_entries(b01, b23);
+    }
+}
+
+// A row's sign/mantissa bytes in the wave's stage slice, after the decode.
+constexpr uint32_t kSmRow = kSlabCols + 16;
+static_assert(16 * kSmRow <= 16 * kSegRow * 4, "they fit the slice");
+
+template <int kWavesWG>
 struct SlabLds {
-    uint16_t lut[2][kLutEntries];                 // 16 KB
-    uint8_t slab[2 * kGatedTileRows * kSlabStride];  // 33 KB
-    LutScratch scratch[2];
+    uint32_t plut[kLutEntries];               // 16 KB, at address 0 (afx_gemv_body.h)
+    uint32_t stage[kWavesWG][16 * kSegRow];   // 6.9 KB a wave
+    LutScratch scratch;
 };
 
-// kWays waves share a block of 32 tokens, each multiplying its share of a
-// slab's 16-column steps: 32 tokens a workgroup (kWays 4), 64 (2) or 128 (1).
-template <int kWays>
-__global__ __launch_bounds__(kSlabThreads, 3) void afx_gated_gemm_kernel(const SlabArgs p) {
-    __shared__ __attribute__((aligned(16))) SlabLds lds;
-    uint8_t *slab = lds.slab;
-    const uint32_t lane = threadIdx.x & (kWave - 1);
+// kTB: token blocks of 16. One workgroup runs on a CU: 16 waves up to 64 tokens
+// (128 registers), 8 above, whose token operands take more of the LDS.
+template <int kTB>
+__global__ __launch_bounds__(gated_waves(kTB) *kWave, gated_waves(kTB) / 4)
+void afx_gated_gemm_kernel(const SlabArgs p) {
+    constexpr int kWavesWG = gated_waves(kTB);
+    __shared__ __attribute__((aligned(16))) SlabLds<kWavesWG> lds;
+    // Where a slab's token operands come from: the L1 (each 16 tokens cost 15
+    // us more on 17408 x 5120: the L1's rate), or LDS, where they are put once
+    // for all waves, which then wait for each other twice a slab (20 us, then
+    // 5 us per 16 tokens). Measured, L1 and LDS: 16 tokens 91 and 111 us, 32 105
+    // and 117, 48 121 and 122, 64 134 and 125.
+    constexpr bool kDirect = kTB <= 3;
+    __shared__ __attribute__((aligned(16))) uint8_t xs[kDirect ? 16 : kSlabSteps * kTB * 1024];
+    const uint32_t lane = threadIdx.x & (kWave - 1), q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t s0 = range_begin(p.split, blockIdx.x), s1 = range_begin(p.split, blockIdx.x + 1);
+    const uint32_t mat = blockIdx.x & 1, range = blockIdx.x >> 1;
+    const TensorDesc T = mat ? p.w[1] : p.w[0];
+    const uint32_t len = threadIdx.x < 256 ? T.code_len[threadIdx.x] : 0u;
+    const uint32_t s0 = range_begin(p.split, range), s1 = range_begin(p.split, range + 1);
 
-    // Restore: this lane's row of the tile (one quad per row) and its groups.
-    const uint32_t q4 = lane & 3, lrow = wave * 16 + (lane >> 2);
-    const uint32_t mat = wave >> 1, mrow = lrow & (kGatedTileRows - 1);
-    const TensorDesc &T = p.w[mat];
-    const uint16_t *lut = lds.lut[mat];
-    uint32_t *seg = reinterpret_cast<uint32_t *>(slab + lrow * kSlabStride);
-    uint8_t *out_row = slab + lrow * kSlabStride;
-    // Multiply: this lane's token and the wave's steps.
-    constexpr uint32_t kSteps = kSlabCols / 16 / kWays;
-    constexpr uint32_t kPre = kWays == 1 ? 5 : kWays == 2 ? kSteps / 2 : kSteps;  // A steps fetched before the restore
-    const uint32_t t_wave = (wave / kWays) * 32, ks0 = kSteps * (wave % kWays);
-    const uint32_t tok = t_wave + (lane & 31);
-    const bool tok_ok = tok < p.m, wave_mul = t_wave < p.m;
-    const uint32_t kx = 16 * ks0 + 8 * (lane >> 5);  // the lane's first column in a slab
-    const uint16_t *xa = p.x + (uint64_t)(tok_ok ? tok : 0) * p.ldx + kx;
-    const uint8_t *b_row0 = slab + (lane & 31) * kSlabStride + 16 * (lane >> 5);
-    const uint8_t *b_row1 = b_row0 + 32 * kSlabStride;
-
-    const uint32_t len0 = p.w[0].code_len[threadIdx.x], len1 = p.w[1].code_len[threadIdx.x];
+    const uint32_t c = lane & 3, lrow = lane >> 2;  // the lane's part and row when loading
+    uint32_t *seg_w = lds.stage[wave] + lrow * kSegRow;
+    const uint32_t *seg = lds.stage[wave] + (lane & 15) * kSegRow;
+    uint8_t *sm_w = reinterpret_cast<uint8_t *>(lds.stage[wave]) + lrow * kSmRow + 16 * c;
+    const uint8_t *sm_r = reinterpret_cast<const uint8_t *>(lds.stage[wave]) + (lane & 15) * kSmRow + kGroup * q;
     uint32_t tile = s0 / p.split.tile_slabs, k0 = (s0 - tile * p.split.tile_slabs) * kSlabCols;
-    uint32_t tile_n = tile, k0_n = k0;  // the slab after
-    if (s0 + 1 < s1) next_slab(p, tile_n, k0_n);
-    Bits bits_c = seg_bits(T, segment(p, tile, k0, mrow, q4));
-    Data data_c = seg_data(T, segment(p, tile, k0, mrow, q4), q4, bits_c);
-    Bits bits_n = seg_bits(T, segment(p, tile_n, k0_n, mrow, q4));
-    build_lut<kSlabThreads>(len0, lds.lut[0], lds.scratch[0]);
-    build_lut<kSlabThreads>(len1, lds.lut[1], lds.scratch[1]);
-    __syncthreads();
-    f32x16 acc[2] = {f32x16{}, f32x16{}};
-    for (uint32_t s = s0; s < s1; ++s) {
-        put_seg4(seg, 4 * q4, data_c.w0);
-        put_seg4(seg, 16 + 4 * q4, data_c.w1);
-        for (uint32_t i = 32 + 4 * q4; i < data_c.nw; i += 16) put_seg4(seg, i, load_words4(T, data_c.wa + i));
-        // the next slab's words, the one after's offsets, this slab's tokens
-        Data data_n = data_c;
-        if (s + 1 < s1) data_n = seg_data(T, segment(p, tile_n, k0_n, mrow, q4), q4, bits_n);
-        Bits bits_nn = bits_n;
-        if (s + 2 < s1) {
-            uint32_t tile_nn = tile_n, k0_nn = k0_n;
-            next_slab(p, tile_nn, k0_nn);
-            bits_nn = seg_bits(T, segment(p, tile_nn, k0_nn, mrow, q4));
+    // The wave's 16 rows of tile t, and the lane's part of a slab. Rows past
+    // the matrix repeat its last ones; their sums are not used.
+    auto rows_of = [&](uint32_t t) { return min(t * p.split.waves + wave, p.split.row_tiles - 1); };
+    auto segment = [&](uint32_t t, uint32_t k) {
+        return Seg{umin32(lrow, p.rows - 1 - rows_of(t) * kGatedWaveRows) * p.cols + k, umin32(kSlabCols, p.cols - k)};
+    };
+    auto next = [&](uint32_t &t, uint32_t &k) {  // the slab after
+        k += kSlabCols;
+        if (k >= p.cols) {
+            k = 0;
+            ++t;
         }
-        bf16x8 xv[kSteps];
-        auto load_step = [&](uint32_t ks) { return load_a(xa + k0 + 16 * ks, tok_ok && k0 + kx + 16 * ks < p.cols); };
-        if (wave_mul) {
+    };
+    uint32_t tile_n = tile, k0_n = k0;  // the slab after
+    if (s0 + 1 < s1) next(tile_n, k0_n);
+    Words words;
+    Bits bits;
+    u32x4 w0, w1, sm[4];  // the lane's 8 of the row's first 32 words; 4 of 16 times 16 sign/mantissa bytes
+    auto load_bits = [&](uint32_t t, uint32_t k) {
+        bits = seg_bits(tile_at(T, rows_of(t), p.cols), segment(t, k), c);
+    };
+    auto load_words = [&] {
+        w0 = __builtin_bit_cast(u32x4, load_words4(T, words.wa + 4 * c));
+        w1 = __builtin_bit_cast(u32x4, load_words4(T, words.wa + 16 + 4 * c));
+    };
+    auto load_sm = [&](uint32_t t, uint32_t k) {  // read once: not kept in the caches
+        const Seg g = segment(t, k);
+        const uint8_t *row = tile_at(T, rows_of(t), p.cols).sm;
 #pragma unroll
-            for (uint32_t ks = 0; ks < kPre; ++ks) xv[ks] = load_step(ks);
+        for (uint32_t i = 0; i < 4; ++i)
+            sm[i] = __builtin_nontemporal_load(
+                reinterpret_cast<const u32x4 *>(row + g.start + min(64 * i + 16 * c, g.len - 16)));
+    };
+    load_bits(tile, k0);
+    words = seg_words_of(bits);
+    load_words();
+    load_bits(tile_n, k0_n);
+    [[clang::always_inline]] build_lut<kWavesWG * kWave, true>(len, lds.plut, lds.scratch);
+    __syncthreads();
+    const bool active = wave < p.split.waves;
+    if (kDirect && !active) return;
+    f32x4 acc[kTB];
+#pragma unroll
+    for (int b = 0; b < kTB; ++b) acc[b] = f32x4{};
+    const auto xrsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t *>(p.xp), (short)0, (int)(p.split.tile_slabs * kSlabSteps * kTB * 1024), 0x00020000);
+    for (uint32_t s = s0; s < s1; ++s) {
+        // The words requested a slab ago (pinned here, or the compiler moves
+        // their reversal, and so the wait for them, up to the request).
+        asm volatile("" : "+v"(w0), "+v"(w1));
+        put_seg4(seg_w, 4 * c, __builtin_bit_cast(uint4, w0));
+        put_seg4(seg_w, 16 + 4 * c, __builtin_bit_cast(uint4, w1));
+        for (uint32_t i = 32 + 4 * c; i < words.nw; i += 16) put_seg4(seg_w, i, load_words4(T, words.wa + i));
+        uint32_t r1, r2;
+        chain_starts(words.starts, lane, r1, r2);
+        if constexpr (!kDirect) {
+            __syncthreads();  // every wave is done with the last slab's token operands
+            for (uint32_t o = wave; o < kSlabSteps * kTB; o += kWavesWG)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    xrsrc, (__attribute__((address_space(3))) void *)(xs + o * 1024), 16,
+                    (int)((k0 / kSlabCols * kSlabSteps * kTB + o) * 1024 + lane * 16), 0, 0, 0);
+        }
+        // All that is requested here arrives while the slab decodes: its
+        // sign/mantissa bytes, the next slab's words, the one after's offsets.
+        load_sm(tile, k0);
+        if (s + 1 < s1) {
+            words = seg_words_of(bits);
+            load_words();
+        }
+        if (s + 2 < s1) {
+            uint32_t t2 = tile_n, k2 = k0_n;
+            next(t2, k2);
+            load_bits(t2, k2);
         }
         wave_sync();
         uint32_t ex1[8], ex2[8];
-        decode_groups(seg, seg_chain_r0(bit1(bits_c), data_c.wa), seg_chain_r0(bit2(bits_c), data_c.wa), lut, ex1,
-                      ex2);
-        wave_sync();  // the row's staged words have been read: its slab row may be written
+        decode_pairs(seg, r1, r2, lds.plut, ex1, ex2);
+        wave_sync();  // the staged words have been read
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) *reinterpret_cast<u32x4 *>(sm_w + 64 * i) = sm[i];
+        wave_sync();
         // columns past the row's end become zeros
-        const uint32_t in1 = k0 + kGroup * q4 < p.cols ? ~0u : 0u, in2 = k0 + kGroup * (q4 + 4) < p.cols ? ~0u : 0u;
-        const uint32_t b1[8] = {data_c.s1a.x, data_c.s1a.y, data_c.s1a.z, data_c.s1a.w,
-                                data_c.s1b.x, data_c.s1b.y, data_c.s1b.z, data_c.s1b.w};
-        const uint32_t b2[8] = {data_c.s2a.x, data_c.s2a.y, data_c.s2a.z, data_c.s2a.w,
-                                data_c.s2b.x, data_c.s2b.y, data_c.s2b.z, data_c.s2b.w};
-        uint4 *o1 = reinterpret_cast<uint4 *>(out_row + 64 * q4);
-        uint4 *o2 = reinterpret_cast<uint4 *>(out_row + 64 * (q4 + 4));
+        const uint32_t in1 = k0 + kGroup * q < p.cols ? ~0u : 0u, in2 = k0 + kGroup * (q + 4) < p.cols ? ~0u : 0u;
+        uint4 wf[kSlabSteps];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint4 v1, v2;
-            join4(b1[2 * j], ex1[2 * j], v1.x, v1.y);
-            join4(b1[2 * j + 1], ex1[2 * j + 1], v1.z, v1.w);
-            join4(b2[2 * j], ex2[2 * j], v2.x, v2.y);
-            join4(b2[2 * j + 1], ex2[2 * j + 1], v2.z, v2.w);
-            o1[j] = make_uint4(v1.x & in1, v1.y & in1, v1.z & in1, v1.w & in1);
-            o2[j] = make_uint4(v2.x & in2, v2.y & in2, v2.z & in2, v2.w & in2);
+        for (int j = 0; j < 4; j += 2) {
+            const uint4 m1 = *reinterpret_cast<const uint4 *>(sm_r + 8 * j);
+            const uint4 m2 = *reinterpret_cast<const uint4 *>(sm_r + 128 + 8 * j);
+            join4(m1.x & in1, ex1[2 * j] & in1, wf[j].x, wf[j].y);
+            join4(m1.y & in1, ex1[2 * j + 1] & in1, wf[j].z, wf[j].w);
+            join4(m1.z & in1, ex1[2 * j + 2] & in1, wf[j + 1].x, wf[j + 1].y);
+            join4(m1.w & in1, ex1[2 * j + 3] & in1, wf[j + 1].z, wf[j + 1].w);
+            join4(m2.x & in2, ex2[2 * j] & in2, wf[4 + j].x, wf[4 + j].y);
+            join4(m2.y & in2, ex2[2 * j + 1] & in2, wf[4 + j].z, wf[4 + j].w);
+            join4(m2.z & in2, ex2[2 * j + 2] & in2, wf[5 + j].x, wf[5 + j].y);
+            join4(m2.w & in2, ex2[2 * j + 3] & in2, wf[5 + j].z, wf[5 + j].w);
         }
-        __syncthreads();  // the slab is complete
-        if (wave_mul) {
+        wave_sync();  // the bytes have been read: the next slab's words may be staged
+        if constexpr (kDirect) {
+            __builtin_amdgcn_sched_barrier(0);  // (not requested before the decode: registers)
+            constexpr uint32_t kAhead = kTB == 1 ? 6 : kTB == 2 ? 3 : kTB == 3 ? 2 : 1;
+            u32x4 xv[kSlabSteps][kTB];
+            auto load_step = [&](uint32_t st) {
 #pragma unroll
-            for (uint32_t ks = 0; ks < kSteps; ++ks) {
-                if (ks + kPre < kSteps) xv[ks + kPre] = load_step(ks + kPre);
-                const uint32_t kb = 32 * (ks0 + ks);
-                const bf16x8 w0 = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(b_row0 + kb));
-                const bf16x8 w1 = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(b_row1 + kb));
-                acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xv[ks], w0, acc[0], 0, 0, 0);
-                acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xv[ks], w1, acc[1], 0, 0, 0);
+                for (int b = 0; b < kTB; ++b)
+                    xv[st][b] = __builtin_amdgcn_raw_buffer_load_b128(
+                        xrsrc, (int)(lane * 16), (int)((k0 / kSlabCols * kSlabSteps * kTB + st * kTB + b) * 1024), 0);
+            };
+#pragma unroll
+            for (uint32_t st = 0; st < kAhead; ++st) load_step(st);
+#pragma unroll
+            for (uint32_t st = 0; st < kSlabSteps; ++st) {
+                if (st + kAhead < kSlabSteps) load_step(st + kAhead);
+                __builtin_amdgcn_sched_barrier(0);  // (the compiler would request them later)
+#pragma unroll
+                for (int b = 0; b < kTB; ++b)
+                    acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, wf[st]), __builtin_bit_cast(bf16x8, xv[st][b]), acc[b], 0, 0, 0);
+            }
+        } else {
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's share of the operands is in LDS
+            __syncthreads();                     // and every wave's
+            if (active) {
+#pragma unroll
+                for (uint32_t st = 0; st < kSlabSteps; ++st)
+#pragma unroll
+                    for (int b = 0; b < kTB; ++b) {
+                        const uint4 xv = *reinterpret_cast<const uint4 *>(xs + (st * kTB + b) * 1024 + lane * 16);
+                        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wf[st]),
+                                                                         __builtin_bit_cast(bf16x8, xv), acc[b], 0, 0, 0);
+                    }
             }
         }
-        __syncthreads();  // every wave is done with the slab and its staged words
-        bits_c = bits_n;
-        bits_n = bits_nn;
-        data_c = data_n;
         const uint32_t tile_c = tile;
         tile = tile_n;
         k0 = k0_n;
-        next_slab(p, tile_n, k0_n);
+        next(tile_n, k0_n);
         if (tile == tile_c && s + 1 < s1) continue;
-        // The tile, or the range, ends: its sums go to their place.
-        if constexpr (kWays > 1) {
-            // the waves that share a token block add up in LDS, in their order
-            static_assert(kWaves * 2 * 16 * kWave * 4 <= sizeof(SlabLds::slab), "partial sums fit the slab");
-            float *mine = reinterpret_cast<float *>(slab) + wave * (2 * 16 * kWave);
-            if (wave_mul && wave % kWays != 0) {
+        // The tile, or the range, ends: its sums go to their place. The
+        // lane's four are rows 4 q .. of token l mod 16.
+        const uint64_t place =
+            part_place(p.split, tile_c, range - range_of(p.split, tile_c * p.split.tile_slabs), wave);
+        f32x4 *out = reinterpret_cast<f32x4 *>(p.part[mat]) + place * kTB * kWave + 4 * (lane & 15) + q;
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    mine[v * kWave + lane] = acc[0][v];
-                    mine[(16 + v) * kWave + lane] = acc[1][v];
-                }
-            }
-            __syncthreads();
-            if (wave % kWays == 0) {
-#pragma unroll
-                for (int w = 1; w < kWays; ++w) {
-                    const float *pw = mine + w * (2 * 16 * kWave);
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        acc[0][v] += pw[v * kWave + lane];
-                        acc[1][v] += pw[(16 + v) * kWave + lane];
-                    }
-                }
-            }
-            __syncthreads();  // before the next slab's words are staged there
+        for (int b = 0; b < kTB; ++b) {
+            if (active) out[b * kWave] = acc[b];
+            acc[b] = f32x4{};
         }
-        if (wave_mul && wave % kWays == 0) {
-            const uint32_t slot = tile_c * p.split.most + (blockIdx.x - range_of(p.split, tile_c * p.split.tile_slabs));
-            uint32_t l = lane;
-            asm volatile("" : "+v"(l));  // (the addresses are not kept in registers through the loop)
-            const uint32_t t0 = t_wave + 4 * (l >> 5);
-            float *out = p.part + ((uint64_t)slot * p.m + t0) * (2 * kGatedTileRows) + (l & 31);
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const uint32_t dt = 8 * (v / 4) + (v & 3);  // accumulator v is token t0 + dt
-                if (t0 + dt < p.m) {
-                    out[dt * (2 * kGatedTileRows)] = acc[0][v];
-                    out[dt * (2 * kGatedTileRows) + kGatedTileRows] = acc[1][v];
-                }
-            }
-        }
-        acc[0] = acc[1] = f32x16{};
     }
 }
 
-// h of one tile and 8 tokens: the tile's ranges in order.
+// h of 16 rows and 16 tokens: the tile's ranges in order.
 template <uint32_t kAct>
 __global__ __launch_bounds__(256) void afx_gated_gemm_join_kernel(const SlabArgs p, const GatedGemm q) {
-    const uint32_t tile = blockIdx.x, t = blockIdx.y * 8 + threadIdx.x / 32, c = threadIdx.x % 32;
-    const uint32_t f = tile * kGatedTileRows + c;
+    const uint32_t tile = blockIdx.x / p.split.waves, wave = blockIdx.x % p.split.waves;
+    const uint32_t f = blockIdx.x * kGatedWaveRows + threadIdx.x % 16, t = blockIdx.y * kTok + threadIdx.x / 16;
     if (t >= p.m || f >= p.rows) return;
     const uint32_t first = range_of(p.split, tile * p.split.tile_slabs);
     const uint32_t n = range_of(p.split, (tile + 1) * p.split.tile_slabs - 1) - first + 1;
     float g = 0.f, u = 0.f;
     for (uint32_t o = 0; o < n; ++o) {
-        const float *v = p.part + (((uint64_t)tile * p.split.most + o) * p.m + t) * (2 * kGatedTileRows) + c;
-        g += v[0];
-        u += v[kGatedTileRows];
+        const uint64_t at = (part_place(p.split, tile, o, wave) * p.blocks + blockIdx.y) * 256 + threadIdx.x;
+        g += p.part[0][at];
+        u += p.part[1][at];
     }
     q.h[(uint64_t)t * q.ldh + f] = __builtin_bit_cast(uint16_t, (__bf16)(act<kAct>(g) * u));
     if (q.g) {
@@ -293,39 +385,62 @@ TensorDesc tensor(const afx_info *info, const void *blob) {
     return t;
 }
 
+uint64_t align_up(uint64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+uint64_t part_bytes(const GatedSplit &s, uint32_t m) {
+    return align_up(part_places(s) * gated_token_blocks(m) * kTok * kGatedWaveRows * 4);
+}
+uint64_t packed_bytes(const GatedSplit &s, uint32_t m) {
+    return (uint64_t)s.tile_slabs * kSlabCols * gated_token_blocks(m) * kTok * 2;
+}
+
+bool launch(const void *fn, dim3 grid, uint32_t threads, void **args, hipStream_t stream) {
+    return hipLaunchKernel(fn, grid, dim3(threads), args, 0, stream) == hipSuccess;
+}
+
 }  // namespace
 
 uint64_t gated_gemm_space(uint64_t rows, uint64_t cols, uint32_t m) {
-    const GatedSplit s = gated_split(rows, cols);
-    return (uint64_t)s.tiles * s.most * m * 2 * kGatedTileRows * 4;
+    const GatedSplit s = gated_split(rows, cols, m);
+    return 2 * part_bytes(s, m) + align_up(packed_bytes(s, m));
 }
 
 int launch_gated_gemm(const afx_gated &w, const GatedGemm &q, uint8_t *ws, hipStream_t stream) {
     SlabArgs p{};
     p.w[0] = tensor(w.gate_info, w.gate_blob_dev);
     p.w[1] = tensor(w.up_info, w.up_blob_dev);
-    p.x = q.x;
-    p.part = reinterpret_cast<float *>(ws);
-    p.ldx = q.ldx;
+    p.split = gated_split(w.rows, w.cols, q.m);
+    const uint64_t pb = part_bytes(p.split, q.m);
+    p.part[0] = reinterpret_cast<float *>(ws);
+    p.part[1] = reinterpret_cast<float *>(ws + pb);
+    uint16_t *packed = reinterpret_cast<uint16_t *>(ws + 2 * pb);
+    p.xp = packed;
     p.m = q.m;
     p.rows = (uint32_t)w.rows;
     p.cols = (uint32_t)w.cols;
-    p.split = gated_split(w.rows, w.cols);
-    const void *fn = q.m <= 32   ? reinterpret_cast<const void *>(&afx_gated_gemm_kernel<4>)
-                     : q.m <= 64 ? reinterpret_cast<const void *>(&afx_gated_gemm_kernel<2>)
-                                 : reinterpret_cast<const void *>(&afx_gated_gemm_kernel<1>);
+    p.blocks = gated_token_blocks(q.m);
+    const uint32_t waves = gated_waves(p.blocks);
+    const uint16_t *x = q.x;
+    uint64_t ldx = q.ldx;
+    void *pack_args[] = {&x, &ldx, &p.m, &p.cols, &p.blocks, &packed};
+    const uint32_t operands = p.split.tile_slabs * kSlabSteps * p.blocks;
+    if (!launch(reinterpret_cast<const void *>(&afx_gated_pack_kernel), dim3((operands + 3) / 4), 256, pack_args, stream))
+        return AFX_E_HIP;
+    const void *fn = p.blocks == 1   ? reinterpret_cast<const void *>(&afx_gated_gemm_kernel<1>)
+                     : p.blocks == 2 ? reinterpret_cast<const void *>(&afx_gated_gemm_kernel<2>)
+                     : p.blocks == 3 ? reinterpret_cast<const void *>(&afx_gated_gemm_kernel<3>)
+                     : p.blocks == 4 ? reinterpret_cast<const void *>(&afx_gated_gemm_kernel<4>)
+                     : p.blocks == 6 ? reinterpret_cast<const void *>(&afx_gated_gemm_kernel<6>)
+                                     : reinterpret_cast<const void *>(&afx_gated_gemm_kernel<8>);
     void *args[] = {&p};
-    if (hipLaunchKernel(fn, dim3(p.split.ranges), dim3(kSlabThreads), args, 0, stream) != hipSuccess) return AFX_E_HIP;
+    if (!launch(fn, dim3(2 * p.split.ranges), waves * kWave, args, stream)) return AFX_E_HIP;
     const void *join = w.act == AFX_ACT_SILU
                            ? reinterpret_cast<const void *>(&afx_gated_gemm_join_kernel<AFX_ACT_SILU>)
                        : w.act == AFX_ACT_GELU_TANH
                            ? reinterpret_cast<const void *>(&afx_gated_gemm_join_kernel<AFX_ACT_GELU_TANH>)
                            : reinterpret_cast<const void *>(&afx_gated_gemm_join_kernel<AFX_ACT_GELU>);
     GatedGemm out = q;
-    void *jargs[] = {&p, &out};
-    return hipLaunchKernel(join, dim3(p.split.tiles, (q.m + 7) / 8), dim3(256), jargs, 0, stream) == hipSuccess
-               ? AFX_OK
-               : AFX_E_HIP;
+    void *join_args[] = {&p, &out};
+    return launch(join, dim3(p.split.row_tiles, p.blocks), 256, join_args, stream) ? AFX_OK : AFX_E_HIP;
 }
 
 }  // namespace afx

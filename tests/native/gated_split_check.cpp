@@ -26,11 +26,14 @@ int g_fail = 0;
         }                                                        \
     } while (0)
 
-void check(uint64_t rows, uint64_t cols, uint32_t resident) {
-    const GatedSplit s = split_slabs(rows, cols, resident);
+void check(uint64_t rows, uint64_t cols, uint32_t resident, uint32_t waves) {
+    const GatedSplit s = split_slabs(rows, cols, resident, waves);
     const uint64_t total = (uint64_t)s.tiles * s.tile_slabs;
-    CHECK((uint64_t)s.tiles * kGatedTileRows >= rows && (uint64_t)s.tile_slabs * kSlabCols >= cols,
+    CHECK((uint64_t)s.tiles * s.waves * kGatedWaveRows >= rows && (uint64_t)s.tile_slabs * kSlabCols >= cols &&
+              (uint64_t)s.row_tiles * kGatedWaveRows >= rows && (s.row_tiles - 1) * (uint64_t)kGatedWaveRows < rows,
           "%llu x %llu not covered", (unsigned long long)rows, (unsigned long long)cols);
+    CHECK(s.waves >= 1 && s.waves <= waves && (s.waves == waves || total < 2ull * resident + s.tile_slabs),
+          "%u waves for %llu slabs", s.waves, (unsigned long long)total);
     CHECK(s.ranges >= 1 && s.ranges <= resident, "%u ranges", s.ranges);
     CHECK(range_begin(s, 0) == 0 && range_begin(s, s.ranges) == total, "ends");
     const uint32_t least = (uint32_t)(total / s.ranges);
@@ -42,6 +45,7 @@ void check(uint64_t rows, uint64_t cols, uint32_t resident) {
             CHECK(range_of(s, i) == w, "slab %u is in range %u, not %u", i, w, range_of(s, i));
             const uint32_t tile = i / s.tile_slabs, place = w - range_of(s, tile * s.tile_slabs);
             CHECK(place < s.most, "tile %u: place %u of %u", tile, place, s.most);
+            CHECK(part_place(s, tile, place, s.waves - 1) < part_places(s), "place past the workspace");
         }
     }
 }
@@ -49,13 +53,14 @@ void check(uint64_t rows, uint64_t cols, uint32_t resident) {
 }  // namespace
 
 int main() {
-    for (uint64_t rows : {1, 5, 31, 32, 33, 64, 100, 1024, 5461, 17408})
+    for (uint64_t rows : {1, 5, 16, 17, 31, 33, 64, 100, 1024, 5461, 17408})
         for (uint64_t cols : {32, 224, 256, 288, 512, 2048, 5120, 17408})
-            for (uint32_t resident : {1, 2, 7, 768}) check(rows, cols, resident);
-    check((1u << 21) - 1, 256, 768);
-    check(1024, (1u << 22) - 32, 768);
+            for (uint32_t resident : {1, 2, 7, 128, 384})
+                for (uint32_t waves : {1, 4, 16}) check(rows, cols, resident, waves);
+    check((1u << 21) - 1, 256, 128, 16);
+    check(1024, (1u << 22) - 32, 384, 4);
     std::mt19937_64 rng(3);
-    for (int i = 0; i < 400; ++i) check(1 + rng() % 40000, 32 * (1 + rng() % 300), 1 + rng() % 1000);
+    for (int i = 0; i < 400; ++i) check(1 + rng() % 40000, 32 * (1 + rng() % 300), 1 + rng() % 500, 1u << rng() % 5);
     if (g_fail) return 1;
     std::puts("gated split ok");
     return 0;

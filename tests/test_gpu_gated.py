@@ -131,7 +131,11 @@ def check(name, got, want, tol):
 # one tile of 128, columns past one of 64 and odd numbers of column tiles
 SIZES = [(1, 8, 1), (5, 8, 2), (3, 72, 3), (130, 136, 4), (128, 64, 5), (257, 200, 7), (64, 264, 31), (131, 5120, 1),
          (96, 4104, 2), (33, 4096, 4), (640, 1024, 33), (129, 328, 64), (100, 1032, 65), (383, 192, 128),
-         (127, 256, 129), (300, 72, 255), (128, 520, 256), (385, 320, 257), (70, 128, 513)]
+         (127, 256, 129), (300, 72, 255), (128, 520, 256), (385, 320, 257), (70, 128, 513),
+         # the fused matrix-core kernel (rows of whole groups): one group a row, rows that end inside a slab, a tile
+         # over many ranges, token counts around every operand count, more slabs than ranges
+         (17, 32, 5), (33, 5120, 6), (100, 2080, 16), (31, 8192, 17), (1000, 288, 32), (2100, 2336, 48),
+         (50, 480, 63), (4000, 2624, 80), (129, 1056, 100), (16, 96, 127), (48, 16384, 128)]
 
 
 @pytest.mark.parametrize("rows,cols,m", SIZES)
@@ -155,7 +159,8 @@ def test_forward(rows, cols, m, act):
     assert torch.equal(only_h[0], h)  # the same bits without g and u, and in another run
 
 
-@pytest.mark.parametrize("rows,cols,m", [(70, 320, 1), (70, 320, 3), (70, 320, 6), (200, 5120, 40), (200, 520, 300)])
+@pytest.mark.parametrize("rows,cols,m", [(70, 320, 1), (70, 320, 3), (70, 320, 6), (200, 5120, 40), (90, 4128, 90),
+                                         (200, 520, 300)])
 def test_forward_integers_exact(rows, cols, m):
     """Small integers: g and u are exact in FP32 whatever the order of the
     sums, so the kept g and u are exactly their BF16 roundings."""
@@ -170,11 +175,11 @@ def test_forward_integers_exact(rows, cols, m):
         assert torch.equal(got, (x64 @ w.T).float().bfloat16().double())
 
 
-@pytest.mark.parametrize("m", [1, 4, 20, 200])
-def test_special_values_stay_where_they_are(m):
+@pytest.mark.parametrize("m,cols", [(1, 200), (4, 200), (20, 200), (20, 224), (100, 288), (200, 200)])
+def test_special_values_stay_where_they_are(m, cols):
     """An infinity in one token and NaN in another reach those tokens only,
     an infinite weight only its own output; large pre-activations saturate."""
-    rows, cols = 40, 200
+    rows = 40
     rng = rng_of(3, m)
     wg, wu = normal(rng, (rows, cols)), normal(rng, (rows, cols))
     wg[5, 3] = np.inf
