@@ -32,11 +32,11 @@ uint64_t align_up(uint64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 struct GradArgs {
     const float *dh;
     const uint16_t *g, *u;
-    uint16_t *dg, *du;  // caller's, may be NULL
-    uint16_t *dgu;      // [m, 2 kpad]: dg, zeros to kpad, du, zeros
+    uint16_t *dg, *du;    // the caller's, or NULL
+    uint16_t *wdg, *wdu;  // [m, kpad] for the product, zeros past the row, or NULL
     uint64_t ldh, ldgu, kpad;
     uint32_t m, rows;
-    uint32_t vec;       // every row starts aligned for four values at once
+    uint32_t vec;         // every row starts aligned for four values at once
 };
 
 __device__ inline float bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -49,7 +49,7 @@ template <uint32_t kAct>
 __global__ __launch_bounds__(256) void afx_gated_grad_kernel(const GradArgs p) {
     const uint32_t f = 4 * (blockIdx.x * 256 + threadIdx.x);
     if (f >= p.kpad) return;
-    for (uint32_t t = blockIdx.y; t < p.m; t += gridDim.y) {
+    for (uint64_t t = blockIdx.y; t < p.m; t += gridDim.y) {
         uint16_t dg[4] = {}, du[4] = {};
         if (f < p.rows) {
             float dh[4] = {}, g[4] = {}, u[4] = {};
@@ -71,22 +71,17 @@ __global__ __launch_bounds__(256) void afx_gated_grad_kernel(const GradArgs p) {
 #pragma unroll
             for (uint32_t i = 0; i < 4; ++i) {
                 float a, da;
-                act_grad<kAct>(g[i], a, da);
+                act_grad<kAct>(g[i], a, da);  // (past the row all three inputs are zero, and so both results)
                 dg[i] = to_bf16(dh[i] * u[i] * da);
                 du[i] = to_bf16(dh[i] * a);
             }
         }
         const uint2 dgv = make_uint2(dg[0] | ((uint32_t)dg[1] << 16), dg[2] | ((uint32_t)dg[3] << 16));
         const uint2 duv = make_uint2(du[0] | ((uint32_t)du[1] << 16), du[2] | ((uint32_t)du[3] << 16));
-        uint16_t *w = p.dgu + (uint64_t)t * 2 * p.kpad + f;  // kpad is a multiple of 64
-        // past the matrix the pad of the reduction is zero
-        auto keep = [&](uint2 v) {
-            if (f + 4 <= p.rows) return v;
-            return make_uint2((f < p.rows ? v.x & 0xFFFFu : 0u) | (f + 1 < p.rows ? v.x & 0xFFFF0000u : 0u),
-                              (f + 2 < p.rows ? v.y & 0xFFFFu : 0u) | (f + 3 < p.rows ? v.y & 0xFFFF0000u : 0u));
-        };
-        *reinterpret_cast<uint2 *>(w) = keep(dgv);
-        *reinterpret_cast<uint2 *>(w + p.kpad) = keep(duv);
+        if (p.wdg) {  // kpad is a multiple of 8; dg and du are zero past the row
+            *reinterpret_cast<uint2 *>(p.wdg + t * p.kpad + f) = dgv;
+            *reinterpret_cast<uint2 *>(p.wdu + t * p.kpad + f) = duv;
+        }
         if (p.dg) {
             uint16_t *a = p.dg + t * p.ldgu + f, *b = p.du + t * p.ldgu + f;
             if (p.vec && f + 4 <= p.rows) {
@@ -159,8 +154,9 @@ GatedPath gated_path(uint64_t cols, uint32_t m) {
 
 // Where the pieces of a gated call's workspace lie, and its size.
 struct GatedSpace {
-    uint64_t wg, wu, dgu, partial, bytes;
+    uint64_t wg, wu, dg, du, partial, bytes;
 };
+uint64_t pad8(uint64_t v) { return (v + 7) / 8 * 8; }
 GatedSpace gated_space(uint64_t rows, uint64_t cols, uint32_t m, bool backward) {
     GatedSpace s{};
     if (m == 0) return s;
@@ -171,9 +167,12 @@ GatedSpace gated_space(uint64_t rows, uint64_t cols, uint32_t m, bool backward) 
     }
     const uint64_t w = align_up(2 * rows * cols);
     s.wu = w;
-    s.dgu = 2 * w;
-    s.partial = s.dgu + (backward ? align_up((uint64_t)m * 4 * mm_pad_k(rows)) : 0);
-    s.bytes = s.partial + (backward ? align_up(mm_transposed_partial(rows, cols, 2, m)) : 0);
+    const uint64_t d = backward ? align_up((uint64_t)m * 2 * pad8(rows)) : 0;
+    s.dg = 2 * w;
+    s.du = s.dg + d;
+    s.partial = s.du + d;
+    s.bytes = s.partial +
+              align_up(backward ? mm_transposed_partial(rows, cols, 2, m) : mm_gated_partial(rows, cols, m));
     return s;
 }
 
@@ -252,6 +251,7 @@ int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_de
     p.g = g_dev;
     p.u = u_dev;
     p.ldgu = gus;
+    p.partial = reinterpret_cast<float *>(ws + sp.partial);
     return launch_mm_gated(p, s);
 }
 
@@ -291,10 +291,17 @@ int afx_restore_gated_backward_async(const afx_gated *w, uint32_t m, const float
     a.u = u_dev;
     a.dg = dg_dev;
     a.du = du_dev;
-    a.dgu = reinterpret_cast<uint16_t *>(ws + sp.dgu);
+    // The product reads the caller's dg and du if their rows are whole
+    // 16-byte pieces, else copies in the workspace.
+    const bool direct = dg_dev && w->rows % 8 == 0 && gu_stride % 8 == 0 && !misaligned(dg_dev, 16) &&
+                        !misaligned(du_dev, 16);
+    if (!direct) {
+        a.wdg = reinterpret_cast<uint16_t *>(ws + sp.dg);
+        a.wdu = reinterpret_cast<uint16_t *>(ws + sp.du);
+    }
     a.ldh = dh_stride;
     a.ldgu = gu_stride;
-    a.kpad = mm_pad_k(w->rows);
+    a.kpad = pad8(w->rows);
     a.m = m;
     a.rows = (uint32_t)w->rows;
     a.vec = dh_stride % 4 == 0 && gu_stride % 4 == 0 && !misaligned(dh_dev, 16) && !misaligned(g_dev, 8) &&
@@ -304,8 +311,9 @@ int afx_restore_gated_backward_async(const afx_gated *w, uint32_t m, const float
     rc = restore_pair(w, ws + sp.wg, ws + sp.wu, s);
     if (rc != AFX_OK) return rc;
     MmTransposed p{};
-    p.a = a.dgu;
-    p.lda = 2 * a.kpad;
+    p.a[0] = direct ? dg_dev : a.wdg;
+    p.a[1] = direct ? du_dev : a.wdu;
+    p.lda = direct ? gu_stride : a.kpad;
     p.m = m;
     p.w[0] = reinterpret_cast<const uint16_t *>(ws + sp.wg);
     p.w[1] = reinterpret_cast<const uint16_t *>(ws + sp.wu);
@@ -348,7 +356,7 @@ int afx_restore_gemm_t_async(const afx_info *info, const void *blob_dev, uint64_
     rc = afx_decode_layer_async(&job, 1, s);
     if (rc != AFX_OK) return rc;
     MmTransposed p{};
-    p.a = d_dev;
+    p.a[0] = d_dev;
     p.lda = rows;
     p.m = m;
     p.w[0] = reinterpret_cast<const uint16_t *>(ws);

@@ -9,12 +9,9 @@
 
 namespace afx {
 
-// Columns of a k-tile, and the multiple to which the reduction of a two-matrix
-// product is padded (so that no k-tile crosses from one matrix to the next).
-constexpr uint32_t kMmTileK = 64;
-constexpr uint64_t mm_pad_k(uint64_t k) { return (k + kMmTileK - 1) / kMmTileK * kMmTileK; }
+constexpr uint32_t kMmTileK = 64;  // reduction steps of a k-tile
 
-// The activation of a gated block (afx_act), as compile-time choice.
+// h = act(x wg^T) * (x wu^T).
 struct MmGated {
     const uint16_t *x;       // BF16 [m, cols], row stride ldx
     uint64_t ldx;
@@ -26,12 +23,13 @@ struct MmGated {
     uint64_t ldh;
     uint16_t *g, *u;         // BF16 [m, rows], row stride ldgu, or NULL
     uint64_t ldgu;
+    float *partial;          // mm_gated_partial(...) bytes
 };
 
-// y = sum over the matrices i of a[:, i kpad .. i kpad + rows) w_i, with
-// kpad = mm_pad_k(rows) when n_mats is 2.
+// y = a[0] w[0] (+ a[1] w[1]).
 struct MmTransposed {
-    const uint16_t *a;       // BF16 [m, n_mats kpad] (one matrix: [m, rows]), row stride lda
+    const uint16_t *a[2];    // BF16 [m, rows], row stride lda, 16-byte aligned rows; rows up to the next
+                             // multiple of 8 are read and must be 0
     uint64_t lda;
     uint32_t m;
     const uint16_t *w[2];    // BF16 [rows, cols], restored
@@ -44,6 +42,7 @@ struct MmTransposed {
     float *partial;          // mm_transposed_partial(...) bytes
 };
 
+uint64_t mm_gated_partial(uint64_t rows, uint64_t cols, uint32_t m);
 uint64_t mm_transposed_partial(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m);
 int launch_mm_gated(const MmGated &p, hipStream_t stream);
 int launch_mm_transposed(const MmTransposed &p, hipStream_t stream);

@@ -44,23 +44,33 @@ constexpr uint32_t kBN = 256;          // weight rows (or columns) of a tile
 constexpr uint32_t kBK = kMmTileK;     // reduction steps of a tile
 constexpr int kBufferFlags = 0x00020000;  // raw buffer, 32-bit data format
 
+// How a launch's tiles are laid out. The tiles of n_full weight tiles (whole
+// rounds of one workgroup per CU) take the whole reduction; those of the
+// n_rest others, which would leave CUs idle in a last round, are cut into
+// `splits` ranges of the reduction, whose sums a second launch adds in order.
+// A unit is a weight tile, or one range of one of the rest; its token tiles
+// follow each other on one XCD, whose L2 then fetches the weights once.
+struct MmPlan {
+    uint32_t m_tiles, n_full, n_rest, splits;
+};
+
 struct MmArgs {
-    const uint16_t *a;      // tokens [m, ak], row stride lda
+    const uint16_t *a0, *a1;  // tokens [m, ak], row stride lda, of each matrix
     const uint16_t *w0, *w1;
     uint64_t lda, ldw;
-    uint32_t m, n;          // tokens; outputs per token
-    uint32_t ak, wk;        // reduction steps held by a; by each matrix
-    uint32_t k_tiles0;      // k-tiles of the first matrix
-    uint32_t k_tiles;       // k-tiles of all matrices
-    uint32_t splits;        // the reduction is cut into this many ranges of k-tiles
-    uint32_t m_tiles, n_tiles;
-    uint16_t *h, *g, *u;    // BF16 outputs
+    uint32_t m, n;            // tokens; outputs per token
+    uint32_t ak, wk;          // reduction steps held by a row of a; by each matrix
+    uint32_t k_tiles0;        // k-tiles of the first matrix
+    uint32_t k_tiles;         // k-tiles of all matrices
+    MmPlan plan;
+    uint16_t *h, *g, *u;      // BF16 outputs
     float *y32;
-    uint64_t ldh, ldgu;     // ldh: also y32's
+    float *partial;           // [n_rest][splits][m_tiles][accumulators of a tile's lanes]
+    uint64_t ldh, ldgu;       // ldh: also y32's
     uint32_t add;
 };
 
-enum MmEpilogue { kEpiGated, kEpiBf16, kEpiF32, kEpiPartial };
+enum MmEpilogue { kEpiGated, kEpiBf16, kEpiF32 };
 
 __device__ inline uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
@@ -87,6 +97,52 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t end) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)end, kBufferFlags);
 }
 
+// The outputs of one 16-token fragment: acc[i] of lane l holds weight rows 16 i
+// + 4 (l / 16) .. + 3 of the wave's 64 and token t.
+template <int kEpi, uint32_t kAct>
+__device__ inline void write_outputs(const MmArgs &p, uint32_t n0, uint32_t wn, uint32_t fk, uint32_t t,
+                                     const f32x4 (&acc)[4]) {
+    if (t >= p.m) return;
+    if constexpr (kEpi == kEpiGated) {
+        const bool vec = ((p.ldh | p.ldgu) & 3) == 0 &&
+                         ((reinterpret_cast<uintptr_t>(p.h) | reinterpret_cast<uintptr_t>(p.g) |
+                           reinterpret_cast<uintptr_t>(p.u)) & 7) == 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t f = n0 + 32 * wn + 16 * i + 4 * fk;
+            if (f >= p.n) continue;
+            const uint32_t n4 = p.n - f;
+            float g[4], u[4], h[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                g[v] = acc[i][v];
+                u[v] = acc[i + 2][v];
+                h[v] = act<kAct>(g[v]) * u[v];
+            }
+            store4(p.h + (uint64_t)t * p.ldh + f, h, n4, vec);
+            if (p.g) {
+                store4(p.g + (uint64_t)t * p.ldgu + f, g, n4, vec);
+                store4(p.u + (uint64_t)t * p.ldgu + f, u, n4, vec);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = n0 + 64 * wn + 16 * i + 4 * fk;
+            if (c >= p.n) continue;  // n is a multiple of 8
+            if constexpr (kEpi == kEpiBf16) {
+                const float v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+                store4(p.h + (uint64_t)t * p.ldh + c, v, 4,
+                       (p.ldh & 3) == 0 && (reinterpret_cast<uintptr_t>(p.h) & 7) == 0);
+            } else {
+                float *y = p.y32 + (uint64_t)t * p.ldh + c;  // 4-byte aligned
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y[v] = p.add ? y[v] + acc[i][v] : acc[i][v];
+            }
+        }
+    }
+}
+
 template <int BM, bool kNN, int kEpi, uint32_t kAct>
 __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
     constexpr int kTokInstr = BM / 64;  // DMA instructions per wave for the token tile
@@ -98,18 +154,18 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
 
     const uint32_t lane = threadIdx.x & (kMmWave - 1);
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kMmWave);
-    // Block b runs on XCD b mod 8: the token tiles of one weight tile follow
-    // each other there, so that its L2 fetches the weights once.
-    const uint32_t xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-    const uint32_t split = idx / (p.m_tiles * ((p.n_tiles + 7) / 8));
-    const uint32_t rest = idx % (p.m_tiles * ((p.n_tiles + 7) / 8));
-    const uint32_t nt = (rest / p.m_tiles) * 8 + xcd;
-    if (nt >= p.n_tiles || split >= p.splits) return;
-    const uint32_t m0 = (rest % p.m_tiles) * BM;
+    // Block b runs on XCD b mod 8.
+    const uint32_t unit = (blockIdx.x >> 3) / p.plan.m_tiles * 8 + (blockIdx.x & 7);
+    const uint32_t mt = (blockIdx.x >> 3) % p.plan.m_tiles, m0 = mt * BM;
+    const bool rest = unit >= p.plan.n_full;
+    const uint32_t r = unit - p.plan.n_full;  // of the rest: weight tile r / splits, range r mod splits
+    if (rest && r >= p.plan.n_rest * p.plan.splits) return;
+    const uint32_t nt = rest ? p.plan.n_full + r / p.plan.splits : unit;
     constexpr uint32_t kOutN = kEpi == kEpiGated ? kBN / 2 : kBN;  // outputs per token of a tile
     const uint32_t n0 = nt * kOutN;
-    const uint32_t kt_lo = (uint32_t)((uint64_t)p.k_tiles * split / p.splits);
-    const uint32_t kt_hi = (uint32_t)((uint64_t)p.k_tiles * (split + 1) / p.splits);
+    const uint32_t splits = rest ? p.plan.splits : 1, split = rest ? r % p.plan.splits : 0;
+    const uint32_t kt_lo = (uint32_t)((uint64_t)p.k_tiles * split / splits);
+    const uint32_t kt_hi = (uint32_t)((uint64_t)p.k_tiles * (split + 1) / splits);
 
     // ---- what this lane loads -------------------------------------------
     // Every buffer resource ends where its rows end: a load past that end
@@ -121,7 +177,7 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
     // rows of 64 k: instruction i covers rows 64 i + 8 wave + lane / 8
     const uint32_t lr = 8 * wave + (lane >> 3);
     const uint32_t lc = (lane & 7) ^ ((lr >> 1) & 7);  // 64 i leaves the swizzle unchanged
-    const uint16_t *a_base = p.a + (uint64_t)m0 * p.lda;
+    const uint64_t a_row = (uint64_t)m0 * p.lda;
     const uint32_t a_end = (uint32_t)(((min((uint32_t)BM, p.m - m0) - 1) * p.lda + p.ak) * 2);
     uint32_t a_off[kTokInstr];
 #pragma unroll
@@ -147,11 +203,12 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
 
     // Request k-tile kt into a buffer.
     auto stage = [&](uint32_t kt, uint8_t *tok, uint8_t *wt) {
-        const uint32_t ak0 = kt * kBK;
+        const bool second = kNN && kt >= p.k_tiles0;
+        const uint32_t k0 = (kt - (second ? p.k_tiles0 : 0u)) * kBK;
         uint8_t *tok_w = tok + wave * 1024, *wt_w = wt + wave * 1024;
-        const auto ra = buffer(a_base, a_end);
+        const auto ra = buffer((second ? p.a1 : p.a0) + a_row, a_end);
         // steps come in whole chunks of 8
-        const uint32_t step = 2 * ak0 + (ak0 + 8 * lc < p.ak ? 0u : kPastEnd);
+        const uint32_t step = 2 * k0 + (k0 + 8 * lc < p.ak ? 0u : kPastEnd);
 #pragma unroll
         for (int i = 0; i < kTokInstr; ++i) load_to_lds(ra, a_off[i] + step, tok_w + i * 8192);
         if constexpr (!kNN) {
@@ -159,8 +216,6 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) load_to_lds(rw, w_off[i] + step, wt_w + i * 8192);
         } else {
-            const bool second = kt >= p.k_tiles0;
-            const uint32_t k0 = (kt - (second ? p.k_tiles0 : 0u)) * kBK;
             const auto rw = buffer((second ? p.w1 : p.w0) + (uint64_t)k0 * p.ldw + n0,
                                    (uint32_t)(((min(kBK, p.wk - k0) - 1) * p.ldw + (p.n - n0)) * 2));
 #pragma unroll
@@ -228,97 +283,85 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
         compute(tok0, wt0);
     }
 
-    // ---- outputs: accumulator v of lane l is weight row 16 i + 4 (l / 16) +
-    // v and token 16 j + l % 16 ------------------------------------------------
+    // ---- outputs, or a range's sums as they lie in the lanes ------------------
+    if (splits == 1) {
 #pragma unroll
-    for (int j = 0; j < kMT; ++j) {
-        const uint32_t t = m0 + (BM / 2) * wm + 16 * j + fr;
-        if (t >= p.m) continue;
-        if constexpr (kEpi == kEpiGated) {
-            const bool vec = ((p.ldh | p.ldgu) & 3) == 0 &&
-                             ((reinterpret_cast<uintptr_t>(p.h) | reinterpret_cast<uintptr_t>(p.g) |
-                               reinterpret_cast<uintptr_t>(p.u)) & 7) == 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t f = n0 + 32 * wn + 16 * i + 4 * fk;
-                if (f >= p.n) continue;
-                const uint32_t n4 = p.n - f;
-                float g[4], u[4], h[4];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    g[v] = acc[i][j][v];
-                    u[v] = acc[i + 2][j][v];
-                    h[v] = act<kAct>(g[v]) * u[v];
-                }
-                store4(p.h + (uint64_t)t * p.ldh + f, h, n4, vec);
-                if (p.g) {
-                    store4(p.g + (uint64_t)t * p.ldgu + f, g, n4, vec);
-                    store4(p.u + (uint64_t)t * p.ldgu + f, u, n4, vec);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t c = n0 + 64 * wn + 16 * i + 4 * fk;
-                if (c >= p.n) continue;  // n is a multiple of 8
-                if constexpr (kEpi == kEpiBf16) {
-                    const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                    store4(p.h + (uint64_t)t * p.ldh + c, v, 4,
-                           (p.ldh & 3) == 0 && (reinterpret_cast<uintptr_t>(p.h) & 7) == 0);
-                } else if constexpr (kEpi == kEpiF32) {
-                    float *y = p.y32 + (uint64_t)t * p.ldh + c;  // 4-byte aligned
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) y[v] = p.add ? y[v] + acc[i][j][v] : acc[i][j][v];
-                } else {  // partial sums of this range, [splits, m, n]
-                    float *y = p.y32 + ((uint64_t)split * p.m + t) * p.n + c;
-                    *reinterpret_cast<f32x4 *>(y) = acc[i][j];
-                }
-            }
+        for (int j = 0; j < kMT; ++j) {
+            const f32x4 v[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
+            write_outputs<kEpi, kAct>(p, n0, wn, fk, m0 + (BM / 2) * wm + 16 * j + fr, v);
         }
+    } else {
+        f32x4 *out = reinterpret_cast<f32x4 *>(p.partial) + ((uint64_t)r * p.plan.m_tiles + mt) * (4 * kMT * kMmThreads);
+#pragma unroll
+        for (int j = 0; j < kMT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[(4 * j + i) * kMmThreads + threadIdx.x] = acc[i][j];
     }
 }
 
-// The partial sums of every range, added in their order: the same result on
-// every run.
-template <bool kBf16>
-__global__ __launch_bounds__(256) void afx_mm_join_kernel(const float *part, uint32_t splits, uint32_t m, uint32_t n,
-                                                          void *out, uint64_t ld, uint32_t add) {
-    const uint64_t total = (uint64_t)m * n;
-    for (uint64_t i = 4 * ((uint64_t)blockIdx.x * 256 + threadIdx.x); i < total; i += 4ull * 256 * gridDim.x) {
-        f32x4 s = *reinterpret_cast<const f32x4 *>(part + i);
-        for (uint32_t k = 1; k < splits; ++k) s += *reinterpret_cast<const f32x4 *>(part + k * total + i);
-        const uint64_t t = i / n, c = i % n;  // n is a multiple of 8: four outputs of one token
-        if constexpr (kBf16) {
-            uint16_t *y = static_cast<uint16_t *>(out) + t * ld + c;
-            for (int v = 0; v < 4; ++v) y[v] = to_bf16(s[v]);
-        } else {
-            float *y = static_cast<float *>(out) + t * ld + c;
-            for (int v = 0; v < 4; ++v) y[v] = add ? y[v] + s[v] : s[v];
+// One 16-token fragment of every wave of one of the rest's tiles: the ranges'
+// sums added in their order (the same bits on every run), then the outputs.
+template <int BM, int kEpi, uint32_t kAct>
+__global__ __launch_bounds__(kMmThreads) void afx_mm_join_kernel(const MmArgs p) {
+    constexpr int kMT = BM / 32;
+    const uint32_t j = blockIdx.x % kMT, mt = blockIdx.x / kMT % p.plan.m_tiles, nr = blockIdx.x / kMT / p.plan.m_tiles;
+    const uint32_t lane = threadIdx.x & (kMmWave - 1), wave = threadIdx.x / kMmWave;
+    f32x4 acc[4];
+    for (uint32_t s = 0; s < p.plan.splits; ++s) {
+        const f32x4 *in = reinterpret_cast<const f32x4 *>(p.partial) +
+                          ((uint64_t)(nr * p.plan.splits + s) * p.plan.m_tiles + mt) * (4 * kMT * kMmThreads);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 v = in[(4 * j + i) * kMmThreads + threadIdx.x];
+            acc[i] = s ? acc[i] + v : v;
         }
     }
+    constexpr uint32_t kOutN = kEpi == kEpiGated ? kBN / 2 : kBN;
+    write_outputs<kEpi, kAct>(p, (p.plan.n_full + nr) * kOutN, wave & 3, lane >> 4,
+                              mt * BM + (BM / 2) * (wave >> 2) + 16 * j + (lane & 15), acc);
 }
+
+// A CU runs one workgroup of these tiles, 32 CUs share an XCD. (On another
+// device the launches do the same work in another number of rounds: the plan,
+// and so the workspace and the order of the sums, do not depend on it.)
+constexpr uint32_t kXcds = 8, kXcdCus = 32;
+constexpr uint32_t kLeastRange = 8;  // k-tiles: a range's start and join take about as long as 4
 
 uint32_t tokens_per_tile(uint32_t m) { return m <= 64 ? 64 : m <= 128 ? 128 : 256; }
 
-// How many ranges the reduction is cut into: as many as still fit one
-// workgroup per CU, each of at least 8 k-tiles.
-uint32_t transposed_splits(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
-    const uint64_t bm = tokens_per_tile(m);
-    const uint64_t tiles = ((m + bm - 1) / bm) * ((cols + kBN - 1) / kBN);
-    const uint64_t k_tiles = n_mats * (mm_pad_k(rows) / kBK);
-    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(256 / tiles, k_tiles / 8));
+MmPlan mm_plan(uint32_t m, uint64_t n, uint32_t out_n, uint64_t k_tiles) {
+    const uint32_t bm = tokens_per_tile(m);
+    MmPlan p{};
+    p.m_tiles = (m + bm - 1) / bm;
+    const uint32_t n_tiles = (uint32_t)((n + out_n - 1) / out_n);
+    // weight tiles of a round: what every XCD's CUs take at once
+    const uint32_t round = kXcds * std::max(1u, kXcdCus / p.m_tiles);
+    p.n_full = n_tiles / round * round;
+    p.n_rest = n_tiles - p.n_full;
+    p.splits = 1;
+    if (p.n_rest == 0) return p;
+    const uint32_t most = (uint32_t)std::max<uint64_t>(1, k_tiles / kLeastRange);
+    while (p.splits < most && (p.n_rest * (p.splits + 1) + kXcds - 1) / kXcds * p.m_tiles <= kXcdCus) ++p.splits;
+    return p;
+}
+
+uint64_t partial_bytes(const MmPlan &p, uint32_t m) {
+    return p.splits > 1 ? (uint64_t)p.n_rest * p.splits * p.m_tiles * tokens_per_tile(m) * kBN * 4 : 0;
 }
 
 template <int BM, bool kNN, int kEpi, uint32_t kAct>
 int launch(MmArgs &p, hipStream_t stream) {
-    const uint32_t out_n = kEpi == kEpiGated ? kBN / 2 : kBN;
-    p.m_tiles = (p.m + BM - 1) / BM;
-    p.n_tiles = (p.n + out_n - 1) / out_n;
-    const uint64_t blocks = (uint64_t)p.m_tiles * ((p.n_tiles + 7) / 8) * 8 * p.splits;
+    const MmPlan &q = p.plan;
+    const uint64_t units = (uint64_t)q.n_full + q.n_rest * q.splits;
+    const uint64_t blocks = (units + kXcds - 1) / kXcds * kXcds * q.m_tiles;
     if (blocks >= (1ull << 31)) return AFX_E_UNSUPPORTED;
     void *args[] = {&p};  // hipLaunchKernel reports this launch's own status
-    return hipLaunchKernel(reinterpret_cast<const void *>(&afx_mm_kernel<BM, kNN, kEpi, kAct>),
-                           dim3((unsigned)blocks), dim3(kMmThreads), args, 0, stream) == hipSuccess
+    if (hipLaunchKernel(reinterpret_cast<const void *>(&afx_mm_kernel<BM, kNN, kEpi, kAct>), dim3((unsigned)blocks),
+                        dim3(kMmThreads), args, 0, stream) != hipSuccess)
+        return AFX_E_HIP;
+    if (q.splits == 1) return AFX_OK;
+    return hipLaunchKernel(reinterpret_cast<const void *>(&afx_mm_join_kernel<BM, kEpi, kAct>),
+                           dim3(q.n_rest * q.m_tiles * (BM / 32)), dim3(kMmThreads), args, 0, stream) == hipSuccess
                ? AFX_OK
                : AFX_E_HIP;
 }
@@ -332,11 +375,24 @@ int launch_for_tokens(MmArgs &p, hipStream_t stream) {
     }
 }
 
+uint64_t k_tiles_of(uint64_t k) { return (k + kBK - 1) / kBK; }
+MmPlan gated_plan(uint64_t rows, uint64_t cols, uint32_t m) { return mm_plan(m, rows, kBN / 2, k_tiles_of(cols)); }
+MmPlan transposed_plan(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
+    return mm_plan(m, cols, kBN, n_mats * k_tiles_of(rows));
+}
+
 }  // namespace
+
+uint64_t mm_gated_partial(uint64_t rows, uint64_t cols, uint32_t m) {
+    return partial_bytes(gated_plan(rows, cols, m), m);
+}
+uint64_t mm_transposed_partial(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
+    return partial_bytes(transposed_plan(rows, cols, n_mats, m), m);
+}
 
 int launch_mm_gated(const MmGated &q, hipStream_t stream) {
     MmArgs p{};
-    p.a = q.x;
+    p.a0 = q.x;
     p.lda = q.ldx;
     p.w0 = q.wg;
     p.w1 = q.wu;
@@ -344,8 +400,9 @@ int launch_mm_gated(const MmGated &q, hipStream_t stream) {
     p.m = q.m;
     p.n = (uint32_t)q.rows;
     p.ak = p.wk = (uint32_t)q.cols;
-    p.k_tiles0 = p.k_tiles = (uint32_t)(mm_pad_k(q.cols) / kBK);
-    p.splits = 1;
+    p.k_tiles0 = p.k_tiles = (uint32_t)k_tiles_of(q.cols);
+    p.plan = gated_plan(q.rows, q.cols, q.m);
+    p.partial = q.partial;
     p.h = q.h;
     p.ldh = q.ldh;
     p.g = q.g;
@@ -358,14 +415,10 @@ int launch_mm_gated(const MmGated &q, hipStream_t stream) {
     }
 }
 
-uint64_t mm_transposed_partial(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
-    const uint32_t s = transposed_splits(rows, cols, n_mats, m);
-    return s > 1 ? (uint64_t)s * m * cols * 4 : 0;
-}
-
 int launch_mm_transposed(const MmTransposed &q, hipStream_t stream) {
     MmArgs p{};
-    p.a = q.a;
+    p.a0 = q.a[0];
+    p.a1 = q.a[1];
     p.lda = q.lda;
     p.w0 = q.w[0];
     p.w1 = q.w[1];
@@ -373,30 +426,16 @@ int launch_mm_transposed(const MmTransposed &q, hipStream_t stream) {
     p.m = q.m;
     p.n = (uint32_t)q.cols;
     p.wk = (uint32_t)q.rows;
-    p.k_tiles0 = (uint32_t)(mm_pad_k(q.rows) / kBK);
+    p.ak = (uint32_t)((q.rows + 7) / 8 * 8);
+    p.k_tiles0 = (uint32_t)k_tiles_of(q.rows);
     p.k_tiles = p.k_tiles0 * q.n_mats;
-    p.ak = q.n_mats == 2 ? p.k_tiles * kBK : (uint32_t)q.rows;
-    p.splits = transposed_splits(q.rows, q.cols, q.n_mats, q.m);
+    p.plan = transposed_plan(q.rows, q.cols, q.n_mats, q.m);
+    p.partial = q.partial;
     p.add = q.add;
+    p.h = q.y16;
+    p.y32 = q.y32;
     p.ldh = q.ldy;
-    if (p.splits == 1) {
-        p.h = q.y16;
-        p.y32 = q.y32;
-        return q.y16 ? launch_for_tokens<true, kEpiBf16>(p, stream) : launch_for_tokens<true, kEpiF32>(p, stream);
-    }
-    p.y32 = q.partial;
-    const int rc = launch_for_tokens<true, kEpiPartial>(p, stream);
-    if (rc != AFX_OK) return rc;
-    const uint64_t quads = (uint64_t)q.m * q.cols / 4;
-    const dim3 grid((unsigned)std::min<uint64_t>((quads + 255) / 256, 4096));
-    const float *part = q.partial;
-    void *out = q.y16 ? static_cast<void *>(q.y16) : static_cast<void *>(q.y32);
-    uint32_t splits = p.splits, m = q.m, n = p.n, add = q.add;
-    uint64_t ld = q.ldy;
-    void *args[] = {&part, &splits, &m, &n, &out, &ld, &add};
-    const void *fn = q.y16 ? reinterpret_cast<const void *>(&afx_mm_join_kernel<true>)
-                           : reinterpret_cast<const void *>(&afx_mm_join_kernel<false>);
-    return hipLaunchKernel(fn, grid, dim3(256), args, 0, stream) == hipSuccess ? AFX_OK : AFX_E_HIP;
+    return q.y16 ? launch_for_tokens<true, kEpiBf16>(p, stream) : launch_for_tokens<true, kEpiF32>(p, stream);
 }
 
 }  // namespace afx
