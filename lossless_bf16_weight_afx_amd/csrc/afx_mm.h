@@ -1,22 +1,21 @@
 // afx_mm.h -- the product of BF16 activations with restored BF16 weights on
 // the matrix cores (afx_mm.hip), as the gated feed-forward block and the
-// transposed product use it. Not installed.
+// transposed product use it. Both come as panels (afx_panels.h). Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
 
-#include "afx_internal.h"
+#include "afx_panels.h"
 
 namespace afx {
 
-constexpr uint32_t kMmTileK = 64;  // reduction steps of a k-tile
+constexpr uint32_t kMmTileK = kPanelCols;  // reduction steps of a k-tile
 
 // h = act(x wg^T) * (x wu^T).
 struct MmGated {
-    const uint16_t *x;       // BF16 [m, cols], row stride ldx
-    uint64_t ldx;
+    const uint16_t *x;       // panels of BF16 [m, cols]
     uint32_t m;
-    const uint16_t *wg, *wu; // BF16 [rows, cols], restored
+    const uint16_t *wg, *wu; // panels of BF16 [rows, cols]
     uint64_t rows, cols;
     uint32_t act;
     uint16_t *h;             // BF16 [m, rows], row stride ldh
@@ -28,11 +27,9 @@ struct MmGated {
 
 // y = a[0] w[0] (+ a[1] w[1]).
 struct MmTransposed {
-    const uint16_t *a[2];    // BF16 [m, rows], row stride lda, 16-byte aligned rows; rows up to the next
-                             // multiple of 8 are read and must be 0
-    uint64_t lda;
+    const uint16_t *a[2];    // panels of BF16 [m, rows]
     uint32_t m;
-    const uint16_t *w[2];    // BF16 [rows, cols], restored
+    const uint16_t *w[2];    // panels of BF16 [rows, cols]
     uint32_t n_mats;
     uint64_t rows, cols;
     float *y32;              // FP32 [m, cols], row stride ldy (one of y32, y16)

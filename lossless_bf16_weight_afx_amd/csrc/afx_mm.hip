@@ -12,7 +12,7 @@
 // LDS, 16 bytes a lane), double-buffered: the next tile is requested right
 // after the barrier that frees its buffer and has a whole tile's matrix
 // instructions to arrive. Weights are the A operand of
-// v_mfma_f32_16x16x32_bf16 and tokens the B operand, so that a lane's four
+// v_mfma_f32_32x32x16_bf16 and tokens the B operand, so that a lane's four
 // accumulators are four consecutive outputs of one token.
 //
 // LDS layouts (the loads write lanes' 16 bytes contiguously, so the order is
@@ -20,13 +20,15 @@
 //   * rows of 64 k (128 bytes): 16-byte chunk c of row r sits at chunk c ^
 //     ((r >> 1) & 7), so that the 16 rows a 16-lane phase reads cover all 64
 //     banks once;
-//   * transposed weights, rows of 256 columns (512 bytes): 32-byte unit q of
-//     row k sits at unit q ^ ((k & 3) | (k >> 1 & 4)); the operand's 8
-//     consecutive k of one column come from two ds_read_b64_tr_b16 (a 16-lane
-//     group reads 4 rows of 16 columns and gets them transposed).
+//   * transposed weights, 4 panels of 64 rows of 64 columns (128 bytes):
+//     32-byte unit q of row k sits at unit q ^ ((k & 2) | (k >> 3 & 1)); the
+//     operand's 8 consecutive k of one column come from two
+//     ds_read_b64_tr_b16 (a 16-lane group reads 4 rows of 16 columns and gets
+//     them transposed).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "afx_act.h"
 #include "afx_mm.h"
@@ -37,6 +39,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMmWave = 64, kMmWaves = 8, kMmThreads = kMmWave * kMmWaves;
@@ -55,11 +58,10 @@ struct MmPlan {
 };
 
 struct MmArgs {
-    const uint16_t *a0, *a1;  // tokens [m, ak], row stride lda, of each matrix
-    const uint16_t *w0, *w1;
-    uint64_t lda, ldw;
+    const uint16_t *a0, *a1;  // tokens' panels, of each matrix
+    const uint16_t *w0, *w1;  // weights' panels
     uint32_t m, n;            // tokens; outputs per token
-    uint32_t ak, wk;          // reduction steps held by a row of a; by each matrix
+    uint32_t rows, panels;    // weight rows; panels of a weight matrix
     uint32_t k_tiles0;        // k-tiles of the first matrix
     uint32_t k_tiles;         // k-tiles of all matrices
     MmPlan plan;
@@ -97,26 +99,27 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t end) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)end, kBufferFlags);
 }
 
-// The outputs of one 16-token fragment: acc[i] of lane l holds weight rows 16 i
-// + 4 (l / 16) .. + 3 of the wave's 64 and token t.
+// The outputs of one 32-token fragment: accumulator v of acc[i] of lane l is
+// weight row 32 i + 8 (v / 4) + 4 (l / 32) + v mod 4 of the wave's 64, and
+// token t (l mod 32 of the fragment).
 template <int kEpi, uint32_t kAct>
-__device__ inline void write_outputs(const MmArgs &p, uint32_t n0, uint32_t wn, uint32_t fk, uint32_t t,
-                                     const f32x4 (&acc)[4]) {
+__device__ inline void write_outputs(const MmArgs &p, uint32_t n0, uint32_t wn, uint32_t half, uint32_t t,
+                                     const f32x16 (&acc)[2]) {
     if (t >= p.m) return;
     if constexpr (kEpi == kEpiGated) {
         const bool vec = ((p.ldh | p.ldgu) & 3) == 0 &&
                          ((reinterpret_cast<uintptr_t>(p.h) | reinterpret_cast<uintptr_t>(p.g) |
                            reinterpret_cast<uintptr_t>(p.u)) & 7) == 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t f = n0 + 32 * wn + 16 * i + 4 * fk;
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t f = n0 + 32 * wn + 8 * q + 4 * half;
             if (f >= p.n) continue;
             const uint32_t n4 = p.n - f;
             float g[4], u[4], h[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                g[v] = acc[i][v];
-                u[v] = acc[i + 2][v];
+                g[v] = acc[0][4 * q + v];
+                u[v] = acc[1][4 * q + v];
                 h[v] = act<kAct>(g[v]) * u[v];
             }
             store4(p.h + (uint64_t)t * p.ldh + f, h, n4, vec);
@@ -127,17 +130,18 @@ __device__ inline void write_outputs(const MmArgs &p, uint32_t n0, uint32_t wn, 
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t c = n0 + 64 * wn + 16 * i + 4 * fk;
+        for (int q = 0; q < 8; ++q) {
+            const uint32_t c = n0 + 64 * wn + 8 * q + 4 * half;
             if (c >= p.n) continue;  // n is a multiple of 8
+            const float v[4] = {acc[q / 4][4 * (q % 4)], acc[q / 4][4 * (q % 4) + 1], acc[q / 4][4 * (q % 4) + 2],
+                                acc[q / 4][4 * (q % 4) + 3]};
             if constexpr (kEpi == kEpiBf16) {
-                const float v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
                 store4(p.h + (uint64_t)t * p.ldh + c, v, 4,
                        (p.ldh & 3) == 0 && (reinterpret_cast<uintptr_t>(p.h) & 7) == 0);
             } else {
                 float *y = p.y32 + (uint64_t)t * p.ldh + c;  // 4-byte aligned
 #pragma unroll
-                for (int v = 0; v < 4; ++v) y[v] = p.add ? y[v] + acc[i][v] : acc[i][v];
+                for (int e = 0; e < 4; ++e) y[e] = p.add ? y[e] + v[e] : v[e];
             }
         }
     }
@@ -146,7 +150,7 @@ __device__ inline void write_outputs(const MmArgs &p, uint32_t n0, uint32_t wn, 
 template <int BM, bool kNN, int kEpi, uint32_t kAct>
 __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
     constexpr int kTokInstr = BM / 64;  // DMA instructions per wave for the token tile
-    constexpr int kMT = BM / 32;        // 16-token fragments per wave
+    constexpr int kMT = BM / 64;        // 32-token fragments per wave
     __shared__ __attribute__((aligned(1024))) uint8_t tok0[BM * kBK * 2];
     __shared__ __attribute__((aligned(1024))) uint8_t tok1[BM * kBK * 2];
     __shared__ __attribute__((aligned(1024))) uint8_t wt0[kBN * kBK * 2];
@@ -168,157 +172,199 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
     const uint32_t kt_hi = (uint32_t)((uint64_t)p.k_tiles * (split + 1) / splits);
 
     // ---- what this lane loads -------------------------------------------
-    // Every buffer resource ends where its rows end: a load past that end
-    // puts zeros into LDS. So tokens past the last, weight rows past the
-    // last and reduction steps past the last (given an offset past every
-    // end) come as zeros, whatever memory holds there. (Columns past the
-    // last of a transposed tile may hold the next row's; they are not stored.)
-    constexpr uint32_t kPastEnd = 0x80000000u;
-    // rows of 64 k: instruction i covers rows 64 i + 8 wave + lane / 8
+    // Every buffer resource ends where its panel does (or further rows of it
+    // do): a load past that end puts zeros into LDS. So tokens past the last
+    // panel's last, weight rows past the last and reduction steps past the
+    // last come as zeros. (Other tokens past the last may be the next panel's;
+    // their outputs are not stored.)
+    // Instruction i of a wave covers rows 64 i + 8 wave + lane / 8 of 128
+    // bytes (transposed weights: rows 8 wave + lane / 8 of panel i).
     const uint32_t lr = 8 * wave + (lane >> 3);
-    const uint32_t lc = (lane & 7) ^ ((lr >> 1) & 7);  // 64 i leaves the swizzle unchanged
-    const uint64_t a_row = (uint64_t)m0 * p.lda;
-    const uint32_t a_end = (uint32_t)(((min((uint32_t)BM, p.m - m0) - 1) * p.lda + p.ak) * 2);
-    uint32_t a_off[kTokInstr];
-#pragma unroll
-    for (int i = 0; i < kTokInstr; ++i) a_off[i] = (uint32_t)((64u * i + lr) * p.lda * 2) + 16 * lc;
-    uint32_t w_off[4];
-    const uint16_t *w_base = nullptr;  // rows contiguous in k: the wave's matrix at row n0
-    uint32_t w_end = 0;
+    const uint32_t off = 128 * lr + 16 * ((lane & 7) ^ ((lr >> 1) & 7));  // 64 i leaves the swizzle unchanged
+    const uint32_t a_end = (uint32_t)((p.m - m0) * 128);
+    uint32_t w_off = off, w_end = 0;
     if constexpr (!kNN) {
         // LDS row 64 i + 8 wave + ..: 32 rows of gate (waves 0-3), then 32 of up
-        w_base = (wave < 4 ? p.w0 : p.w1) + (uint64_t)n0 * p.ldw;
-        w_end = (uint32_t)(((min(kBN / 2, p.n - n0) - 1) * p.ldw + p.wk) * 2);
-        const uint32_t r = 8 * (wave & 3) + (lane >> 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w_off[i] = (uint32_t)((32u * i + r) * p.ldw * 2) + 16 * lc;
+        w_off = 128 * (8 * (wave & 3) + (lane >> 3)) + 16 * ((lane & 7) ^ ((lr >> 1) & 7));
+        w_end = (p.n - n0) * 128;
     } else {
-        // rows of 256 columns: instruction i covers rows 16 i + 2 wave + lane / 32
-        const uint32_t wk_row = 2 * wave + (lane >> 5);
-        const uint32_t sw = (wk_row & 3) | ((wk_row >> 1) & 4);
-        const uint32_t c = ((((lane & 31) >> 1) ^ sw) << 1) | (lane & 1);  // 8-column chunk
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w_off[i] = (uint32_t)((16u * i + wk_row) * p.ldw * 2) + 16 * c;
+        // 32-byte unit (lane & 7) / 2 of row lr takes another unit's place
+        const uint32_t sw = (lr & 2) | ((lr >> 3) & 1);
+        w_off = 128 * lr + 32 * (((lane & 7) >> 1) ^ sw) + 16 * (lane & 1);
     }
 
     // Request k-tile kt into a buffer.
     auto stage = [&](uint32_t kt, uint8_t *tok, uint8_t *wt) {
         const bool second = kNN && kt >= p.k_tiles0;
-        const uint32_t k0 = (kt - (second ? p.k_tiles0 : 0u)) * kBK;
+        const uint32_t panel = kt - (second ? p.k_tiles0 : 0u);
         uint8_t *tok_w = tok + wave * 1024, *wt_w = wt + wave * 1024;
-        const auto ra = buffer((second ? p.a1 : p.a0) + a_row, a_end);
-        // steps come in whole chunks of 8
-        const uint32_t step = 2 * k0 + (k0 + 8 * lc < p.ak ? 0u : kPastEnd);
+        const auto ra = buffer((second ? p.a1 : p.a0) + ((uint64_t)panel * p.m + m0) * kBK, a_end);
 #pragma unroll
-        for (int i = 0; i < kTokInstr; ++i) load_to_lds(ra, a_off[i] + step, tok_w + i * 8192);
+        for (int i = 0; i < kTokInstr; ++i) load_to_lds(ra, off + i * 8192, tok_w + i * 8192);
         if constexpr (!kNN) {
-            const auto rw = buffer(w_base, w_end);
+            const auto rw = buffer((wave < 4 ? p.w0 : p.w1) + ((uint64_t)panel * p.rows + n0) * kBK, w_end);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_to_lds(rw, w_off[i] + step, wt_w + i * 8192);
+            for (int i = 0; i < 4; ++i) load_to_lds(rw, w_off + i * 4096, wt_w + i * 8192);
         } else {
-            const auto rw = buffer((second ? p.w1 : p.w0) + (uint64_t)k0 * p.ldw + n0,
-                                   (uint32_t)(((min(kBK, p.wk - k0) - 1) * p.ldw + (p.n - n0)) * 2));
+            const uint16_t *w = second ? p.w1 : p.w0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_to_lds(rw, w_off[i], wt_w + i * 8192);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t col = n0 / kBK + i;  // the panel of these columns
+                const auto rw = buffer(w + ((uint64_t)min(col, p.panels - 1) * p.rows + panel * kBK) * kBK,
+                                       col < p.panels ? (p.rows - panel * kBK) * 128 : 0u);
+                load_to_lds(rw, w_off, wt_w + i * 8192);
+            }
         }
     };
 
     // ---- what this lane multiplies ----------------------------------------
     const uint32_t wn = wave & 3, wm = wave >> 2;  // the wave's 64 weight rows and BM / 2 tokens
-    const uint32_t fr = lane & 15, fk = lane >> 4;
-    f32x4 acc[4][kMT];
+    const uint32_t fr = lane & 31, half = lane >> 5;
+    f32x16 acc[2][kMT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < kMT; ++j) acc[i][j] = f32x4{};
-    auto frag = [&](const uint8_t *tile, uint32_t row, uint32_t ks) {
-        const uint32_t c = (4 * ks + fk) ^ ((row >> 1) & 7);
+        for (int j = 0; j < kMT; ++j) acc[i][j] = f32x16{};
+    // Row row0 + l mod 32, 8 of the tile's steps from 16 ks + 8 (l / 32).
+    auto frag = [&](const uint8_t *tile, uint32_t row0, uint32_t ks) {
+        const uint32_t row = row0 + fr, c = (2 * ks + half) ^ ((row >> 1) & 7);
         return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(tile + row * 128 + 16 * c));
     };
-    auto frag_t = [&](uint8_t *tile, uint32_t col0, uint32_t ks) {  // 8 k of column col0 + lane % 16
-        const uint32_t k = 32 * ks + 8 * fk + (fr >> 2);
-        const uint32_t unit = (col0 >> 4) ^ ((k & 3) | ((k >> 1) & 4));
-        uint8_t *q = tile + k * 512 + 32 * unit + 8 * (fr & 3);
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)q);
-        const s16x4 hi =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(q + 4 * 512));
+    // The same of columns l mod 32 and 32 + l mod 32 of the wave's panel of a
+    // transposed tile. (The four reads and their wait are one block: through
+    // the compiler's builtin, every transposing read would wait for all loads
+    // into LDS, whichever buffer they fill.)
+    auto frags_t = [&](uint8_t *tile, uint32_t ks, bf16x8 (&f)[2]) {
+        const uint32_t k = 16 * ks + 8 * half + ((lane & 15) >> 2);
+        const uint32_t unit = (lane >> 4) & 1, sw = (k & 2) | ((k >> 3) & 1);
+        const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)tile + wn * 8192 +
+                            k * 128 + 8 * (lane & 3);
+        s16x4 v0, v1, v2, v3;
+        asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
+                     "ds_read_b64_tr_b16 %1, %4 offset:512\n\t"
+                     "ds_read_b64_tr_b16 %2, %5\n\t"
+                     "ds_read_b64_tr_b16 %3, %5 offset:512\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3)
+                     : "v"(at + 32 * (unit ^ sw)), "v"(at + 32 * ((unit + 2) ^ sw))
+                     : "memory");
         typedef short s16x8 __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        f[0] = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+        f[1] = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(v2, v3, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    auto compute = [&](uint8_t *tok, uint8_t *wt) {
+    // A k-tile is 4 kMT slots: slot j of step ks (16 of the tile's 64)
+    // multiplies token fragment j with the step's two weight fragments. Its
+    // fragments were read kLead slots before, so that the matrix cores need
+    // not wait for LDS; the last kLead slots read the next tile's first
+    // fragments. Before those, the tile is done with its buffers.
+    constexpr int kSlots = 4 * kMT, kLead = kMT > 3 ? 3 : kMT, kRing = 4;
+    bf16x8 w[2][2], t[kRing];  // weight fragments of two steps; a ring of token fragments
+    // What slot n (of this tile, or past kSlots of the next) multiplies.
+    auto read = [&](int n, uint8_t *tok, uint8_t *wt) {
+        const int ks = n / kMT, j = n % kMT;
+        t[n % kRing] = frag(tok, (BM / 2) * wm + 32 * j, ks % 4);
+        if (j == 0) {
+            if constexpr (kNN) {
+                frags_t(wt, ks % 4, w[ks % 2]);
+            } else {
 #pragma unroll
-        for (uint32_t ks = 0; ks < kBK / 32; ++ks) {
-            bf16x8 w[4], t[kMT];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = kNN ? frag_t(wt, 64 * wn + 16 * i, ks) : frag(wt, 64 * wn + 16 * i + fr, ks);
-#pragma unroll
-            for (int j = 0; j < kMT; ++j) t[j] = frag(tok, (BM / 2) * wm + 16 * j + fr, ks);
-#pragma unroll
-            for (int j = 0; j < kMT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], t[j], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);  // one step's operands at a time: both do not fit the registers
+                for (int i = 0; i < 2; ++i) w[ks % 2][i] = frag(wt, 64 * wn + 32 * i, ks % 4);
+            }
         }
     };
-    // Every wave's loads into the buffer to be read have landed, and every
-    // wave is done with the other one.
-    auto tile_ready = [&] {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-        __syncthreads();
+    // Slot s of the tile in tok, wt; tok_n, wt_n: the next tile's, if there is one.
+    auto slot = [&](int s, uint8_t *tok, uint8_t *wt, uint8_t *tok_n, uint8_t *wt_n, auto has_next) {
+        const int n = s + kLead;  // the slot whose fragments are read now
+        if (n < kSlots)
+            read(n, tok, wt);
+        else if (has_next)
+            read(n, tok_n, wt_n);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            acc[i][s % kMT] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[s / kMT % 2][i], t[s % kRing], acc[i][s % kMT], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
     };
-
+    auto first_slots = [&](uint8_t *tok, uint8_t *wt) {
+#pragma unroll
+        for (int s = 0; s < kSlots - kLead; ++s) slot(s, tok, wt, tok, wt, std::false_type{});
+    };
+    // The last slots of k-tile kt and the first of the next.
+    auto on_to_next = [&](uint32_t kt, uint8_t *tok, uint8_t *wt, uint8_t *tok_n, uint8_t *wt_n) {
+        // This wave holds all it reads of the tile, and its loads of the next
+        // one have landed; then every wave's.
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __syncthreads();
+        if (kt + 2 < kt_hi) stage(kt + 2, tok, wt);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = kSlots - kLead; s < kSlots; ++s) slot(s, tok, wt, tok_n, wt_n, std::true_type{});
+        first_slots(tok_n, wt_n);
+    };
+    auto last_slots = [&](uint8_t *tok, uint8_t *wt) {
+#pragma unroll
+        for (int s = kSlots - kLead; s < kSlots; ++s) slot(s, tok, wt, tok, wt, std::false_type{});
+    };
     stage(kt_lo, tok0, wt0);
-    for (uint32_t kt = kt_lo; kt + 1 < kt_hi; kt += 2) {
-        tile_ready();
-        stage(kt + 1, tok1, wt1);
-        compute(tok0, wt0);
-        tile_ready();
-        if (kt + 2 < kt_hi) stage(kt + 2, tok0, wt0);
-        compute(tok1, wt1);
+    if (kt_lo + 1 < kt_hi) stage(kt_lo + 1, tok1, wt1);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kLead; ++n) read(n, tok0, wt0);
+    first_slots(tok0, wt0);
+    uint32_t kt = kt_lo;
+    for (; kt + 2 < kt_hi; kt += 2) {
+        on_to_next(kt, tok0, wt0, tok1, wt1);
+        on_to_next(kt + 1, tok1, wt1, tok0, wt0);
     }
-    if ((kt_hi - kt_lo) & 1) {
-        tile_ready();
-        compute(tok0, wt0);
+    if (kt + 1 < kt_hi) {
+        on_to_next(kt, tok0, wt0, tok1, wt1);
+        last_slots(tok1, wt1);
+    } else {
+        last_slots(tok0, wt0);
     }
 
     // ---- outputs, or a range's sums as they lie in the lanes ------------------
     if (splits == 1) {
 #pragma unroll
         for (int j = 0; j < kMT; ++j) {
-            const f32x4 v[4] = {acc[0][j], acc[1][j], acc[2][j], acc[3][j]};
-            write_outputs<kEpi, kAct>(p, n0, wn, fk, m0 + (BM / 2) * wm + 16 * j + fr, v);
+            const f32x16 v[2] = {acc[0][j], acc[1][j]};
+            write_outputs<kEpi, kAct>(p, n0, wn, half, m0 + (BM / 2) * wm + 32 * j + fr, v);
         }
     } else {
-        f32x4 *out = reinterpret_cast<f32x4 *>(p.partial) + ((uint64_t)r * p.plan.m_tiles + mt) * (4 * kMT * kMmThreads);
+        f32x4 *out = reinterpret_cast<f32x4 *>(p.partial) + ((uint64_t)r * p.plan.m_tiles + mt) * (8 * kMT * kMmThreads);
 #pragma unroll
         for (int j = 0; j < kMT; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[(4 * j + i) * kMmThreads + threadIdx.x] = acc[i][j];
+            for (int q = 0; q < 8; ++q) {
+                const f32x16 &v = acc[q / 4][j];
+                out[(8 * j + q) * kMmThreads + threadIdx.x] =
+                    f32x4{v[4 * (q % 4)], v[4 * (q % 4) + 1], v[4 * (q % 4) + 2], v[4 * (q % 4) + 3]};
+            }
     }
 }
 
-// One 16-token fragment of every wave of one of the rest's tiles: the ranges'
+// One 32-token fragment of every wave of one of the rest's tiles: the ranges'
 // sums added in their order (the same bits on every run), then the outputs.
 template <int BM, int kEpi, uint32_t kAct>
 __global__ __launch_bounds__(kMmThreads) void afx_mm_join_kernel(const MmArgs p) {
-    constexpr int kMT = BM / 32;
+    constexpr int kMT = BM / 64;
     const uint32_t j = blockIdx.x % kMT, mt = blockIdx.x / kMT % p.plan.m_tiles, nr = blockIdx.x / kMT / p.plan.m_tiles;
     const uint32_t lane = threadIdx.x & (kMmWave - 1), wave = threadIdx.x / kMmWave;
-    f32x4 acc[4];
+    f32x16 acc[2] = {f32x16{}, f32x16{}};
     for (uint32_t s = 0; s < p.plan.splits; ++s) {
         const f32x4 *in = reinterpret_cast<const f32x4 *>(p.partial) +
-                          ((uint64_t)(nr * p.plan.splits + s) * p.plan.m_tiles + mt) * (4 * kMT * kMmThreads);
+                          ((uint64_t)(nr * p.plan.splits + s) * p.plan.m_tiles + mt) * (8 * kMT * kMmThreads);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f32x4 v = in[(4 * j + i) * kMmThreads + threadIdx.x];
-            acc[i] = s ? acc[i] + v : v;
+        for (int q = 0; q < 8; ++q) {
+            const f32x4 v = in[(8 * j + q) * kMmThreads + threadIdx.x];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[q / 4][4 * (q % 4) + e] += v[e];
         }
     }
     constexpr uint32_t kOutN = kEpi == kEpiGated ? kBN / 2 : kBN;
-    write_outputs<kEpi, kAct>(p, (p.plan.n_full + nr) * kOutN, wave & 3, lane >> 4,
-                              mt * BM + (BM / 2) * (wave >> 2) + 16 * j + (lane & 15), acc);
+    write_outputs<kEpi, kAct>(p, (p.plan.n_full + nr) * kOutN, wave & 3, lane >> 5,
+                              mt * BM + (BM / 2) * (wave >> 2) + 32 * j + (lane & 31), acc);
 }
 
 // A CU runs one workgroup of these tiles, 32 CUs share an XCD. (On another
@@ -361,7 +407,7 @@ int launch(MmArgs &p, hipStream_t stream) {
         return AFX_E_HIP;
     if (q.splits == 1) return AFX_OK;
     return hipLaunchKernel(reinterpret_cast<const void *>(&afx_mm_join_kernel<BM, kEpi, kAct>),
-                           dim3(q.n_rest * q.m_tiles * (BM / 32)), dim3(kMmThreads), args, 0, stream) == hipSuccess
+                           dim3(q.n_rest * q.m_tiles * (BM / 64)), dim3(kMmThreads), args, 0, stream) == hipSuccess
                ? AFX_OK
                : AFX_E_HIP;
 }
@@ -375,10 +421,9 @@ int launch_for_tokens(MmArgs &p, hipStream_t stream) {
     }
 }
 
-uint64_t k_tiles_of(uint64_t k) { return (k + kBK - 1) / kBK; }
-MmPlan gated_plan(uint64_t rows, uint64_t cols, uint32_t m) { return mm_plan(m, rows, kBN / 2, k_tiles_of(cols)); }
+MmPlan gated_plan(uint64_t rows, uint64_t cols, uint32_t m) { return mm_plan(m, rows, kBN / 2, panel_count(cols)); }
 MmPlan transposed_plan(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
-    return mm_plan(m, cols, kBN, n_mats * k_tiles_of(rows));
+    return mm_plan(m, cols, kBN, n_mats * panel_count(rows));
 }
 
 }  // namespace
@@ -393,14 +438,11 @@ uint64_t mm_transposed_partial(uint64_t rows, uint64_t cols, uint32_t n_mats, ui
 int launch_mm_gated(const MmGated &q, hipStream_t stream) {
     MmArgs p{};
     p.a0 = q.x;
-    p.lda = q.ldx;
     p.w0 = q.wg;
     p.w1 = q.wu;
-    p.ldw = q.cols;
     p.m = q.m;
-    p.n = (uint32_t)q.rows;
-    p.ak = p.wk = (uint32_t)q.cols;
-    p.k_tiles0 = p.k_tiles = (uint32_t)k_tiles_of(q.cols);
+    p.n = p.rows = (uint32_t)q.rows;
+    p.k_tiles0 = p.k_tiles = p.panels = (uint32_t)panel_count(q.cols);
     p.plan = gated_plan(q.rows, q.cols, q.m);
     p.partial = q.partial;
     p.h = q.h;
@@ -419,15 +461,13 @@ int launch_mm_transposed(const MmTransposed &q, hipStream_t stream) {
     MmArgs p{};
     p.a0 = q.a[0];
     p.a1 = q.a[1];
-    p.lda = q.lda;
     p.w0 = q.w[0];
     p.w1 = q.w[1];
-    p.ldw = q.cols;
     p.m = q.m;
     p.n = (uint32_t)q.cols;
-    p.wk = (uint32_t)q.rows;
-    p.ak = (uint32_t)((q.rows + 7) / 8 * 8);
-    p.k_tiles0 = (uint32_t)k_tiles_of(q.rows);
+    p.rows = (uint32_t)q.rows;
+    p.panels = (uint32_t)panel_count(q.cols);
+    p.k_tiles0 = (uint32_t)panel_count(q.rows);
     p.k_tiles = p.k_tiles0 * q.n_mats;
     p.plan = transposed_plan(q.rows, q.cols, q.n_mats, q.m);
     p.partial = q.partial;
