@@ -33,8 +33,8 @@ struct GradArgs {
     const float *dh;
     const uint16_t *g, *u;
     uint16_t *dg, *du;    // the caller's, or NULL
-    uint16_t *pdg, *pdu;  // panels for the product
-    uint64_t ldh, ldgu;
+    uint16_t *wdg, *wdu;  // [m, padded] for the product, zeros past the row, or NULL
+    uint64_t ldh, ldgu, padded;
     uint32_t m, rows;
     uint32_t vec;         // every row starts aligned for four values at once
 };
@@ -48,7 +48,7 @@ __device__ inline uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t
 template <uint32_t kAct>
 __global__ __launch_bounds__(256) void afx_gated_grad_kernel(const GradArgs p) {
     const uint32_t f = 4 * (blockIdx.x * 256 + threadIdx.x);
-    if (f >= (p.rows + kPanelCols - 1) / kPanelCols * kPanelCols) return;
+    if (f >= p.padded) return;
     for (uint64_t t = blockIdx.y; t < p.m; t += gridDim.y) {
         uint16_t dg[4] = {}, du[4] = {};
         if (f < p.rows) {
@@ -78,9 +78,10 @@ __global__ __launch_bounds__(256) void afx_gated_grad_kernel(const GradArgs p) {
         }
         const uint2 dgv = make_uint2(dg[0] | ((uint32_t)dg[1] << 16), dg[2] | ((uint32_t)dg[3] << 16));
         const uint2 duv = make_uint2(du[0] | ((uint32_t)du[1] << 16), du[2] | ((uint32_t)du[3] << 16));
-        const uint64_t at = ((f / kPanelCols) * (uint64_t)p.m + t) * kPanelCols + f % kPanelCols;
-        *reinterpret_cast<uint2 *>(p.pdg + at) = dgv;  // zeros past the row
-        *reinterpret_cast<uint2 *>(p.pdu + at) = duv;
+        if (p.wdg) {  // (padded is a multiple of 8)
+            *reinterpret_cast<uint2 *>(p.wdg + t * p.padded + f) = dgv;
+            *reinterpret_cast<uint2 *>(p.wdu + t * p.padded + f) = duv;
+        }
         if (p.dg) {
             uint16_t *a = p.dg + t * p.ldgu + f, *b = p.du + t * p.ldgu + f;
             if (p.vec && f + 4 <= p.rows) {
@@ -101,7 +102,7 @@ int launch_grad(const GradArgs &p, uint32_t act, hipStream_t stream) {
     const void *fn = act == AFX_ACT_SILU        ? reinterpret_cast<const void *>(&afx_gated_grad_kernel<AFX_ACT_SILU>)
                      : act == AFX_ACT_GELU_TANH ? reinterpret_cast<const void *>(&afx_gated_grad_kernel<AFX_ACT_GELU_TANH>)
                                                 : reinterpret_cast<const void *>(&afx_gated_grad_kernel<AFX_ACT_GELU>);
-    const dim3 grid((unsigned)((panel_count(p.rows) * kPanelCols / 4 + 255) / 256), std::min(p.m, 32768u));
+    const dim3 grid((unsigned)((p.padded / 4 + 255) / 256), std::min(p.m, 32768u));
     return hipLaunchKernel(fn, grid, dim3(256), args, 0, stream) == hipSuccess ? AFX_OK : AFX_E_HIP;
 }
 
@@ -153,8 +154,9 @@ GatedPath gated_path(uint64_t cols, uint32_t m) {
 
 // Where the pieces of a gated call's workspace lie, and its size.
 struct GatedSpace {
-    uint64_t wg, wu, a0, a1, partial, bytes;  // a0: x; or dg, and a1: du
+    uint64_t wg, wu, a0, a1, partial, bytes;  // a0: x as panels; or dg, and a1: du
 };
+uint64_t pad8(uint64_t v) { return (v + 7) / 8 * 8; }
 GatedSpace gated_space(uint64_t rows, uint64_t cols, uint32_t m, bool backward) {
     GatedSpace s{};
     if (m == 0) return s;
@@ -163,7 +165,8 @@ GatedSpace gated_space(uint64_t rows, uint64_t cols, uint32_t m, bool backward) 
         s.bytes = path == kPathGemv ? gated_gemv_space(rows, cols, m) : gated_gemm_space(rows, cols, m);
         return s;
     }
-    const uint64_t w = align_up(panel_bytes(rows, cols)), a = align_up(panel_bytes(m, backward ? rows : cols));
+    const uint64_t w = align_up(backward ? 2 * rows * cols : panel_bytes(rows, cols));
+    const uint64_t a = align_up(backward ? 2 * m * pad8(rows) : panel_bytes(m, cols));
     s.wu = w;
     s.a0 = 2 * w;
     s.a1 = s.a0 + (backward ? a : 0);
@@ -184,12 +187,6 @@ int check_gated(const afx_gated *w, uint32_t m) {
 }
 
 uint16_t *u16_at(void *ws, uint64_t at) { return reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + at); }
-
-int restore_pair(const afx_gated *w, void *ws, const GatedSpace &sp, hipStream_t s) {
-    const PanelJob jobs[2] = {{w->gate_info, w->gate_blob_dev, w->rows, w->cols, u16_at(ws, sp.wg)},
-                              {w->up_info, w->up_blob_dev, w->rows, w->cols, u16_at(ws, sp.wu)}};
-    return launch_restore_panels(jobs, 2, s);
-}
 
 }  // namespace
 }  // namespace afx
@@ -234,7 +231,9 @@ int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_de
     const GatedPath path = gated_path(w->cols, m);
     if (path == kPathGemv) return launch_gated_gemv(*w, {x_dev, x_stride, m, h_dev, g_dev, u_dev, h_stride, gus}, ws, s);
     if (path == kPathGemm) return launch_gated_gemm(*w, {x_dev, x_stride, m, h_dev, g_dev, u_dev, h_stride, gus}, ws, s);
-    rc = restore_pair(w, ws, sp, s);
+    const PanelJob jobs[2] = {{w->gate_info, w->gate_blob_dev, w->rows, w->cols, u16_at(ws, sp.wg)},
+                              {w->up_info, w->up_blob_dev, w->rows, w->cols, u16_at(ws, sp.wu)}};
+    rc = launch_restore_panels(jobs, 2, s);
     if (rc != AFX_OK) return rc;
     rc = launch_pack_panels(x_dev, x_stride, m, w->cols, u16_at(ws, sp.a0), s);
     if (rc != AFX_OK) return rc;
@@ -291,21 +290,32 @@ int afx_restore_gated_backward_async(const afx_gated *w, uint32_t m, const float
     a.u = u_dev;
     a.dg = dg_dev;
     a.du = du_dev;
-    a.pdg = u16_at(ws, sp.a0);
-    a.pdu = u16_at(ws, sp.a1);
+    // The product reads the caller's dg and du if their rows are whole
+    // 16-byte pieces, else copies in the workspace.
+    const bool direct = dg_dev && w->rows % 8 == 0 && gu_stride % 8 == 0 && !misaligned(dg_dev, 16) &&
+                        !misaligned(du_dev, 16);
+    if (!direct) {
+        a.wdg = u16_at(ws, sp.a0);
+        a.wdu = u16_at(ws, sp.a1);
+    }
     a.ldh = dh_stride;
     a.ldgu = gu_stride;
+    a.padded = pad8(w->rows);
     a.m = m;
     a.rows = (uint32_t)w->rows;
     a.vec = dh_stride % 4 == 0 && gu_stride % 4 == 0 && !misaligned(dh_dev, 16) && !misaligned(g_dev, 8) &&
             !misaligned(u_dev, 8) && !misaligned(dg_dev, 8) && !misaligned(du_dev, 8);
     rc = launch_grad(a, w->act, s);
     if (rc != AFX_OK) return rc;
-    rc = restore_pair(w, ws, sp, s);
+    const size_t bytes = 2 * w->rows * w->cols;
+    const afx_job jobs[2] = {{w->gate_info, w->gate_blob_dev, u16_at(ws, sp.wg), bytes},
+                             {w->up_info, w->up_blob_dev, u16_at(ws, sp.wu), bytes}};
+    rc = afx_decode_layer_async(jobs, 2, s);
     if (rc != AFX_OK) return rc;
     MmTransposed p{};
-    p.a[0] = a.pdg;
-    p.a[1] = a.pdu;
+    p.a[0] = direct ? dg_dev : a.wdg;
+    p.a[1] = direct ? du_dev : a.wdu;
+    p.lda = direct ? gu_stride : a.padded;
     p.m = m;
     p.w[0] = u16_at(ws, sp.wg);
     p.w[1] = u16_at(ws, sp.wu);
@@ -323,9 +333,7 @@ int afx_restore_gemm_t_workspace(uint64_t rows, uint64_t cols, uint32_t m, size_
     const int rc = check_sizes(rows, cols, m);
     if (rc != AFX_OK) return rc;
     if (rows % 8) return AFX_E_UNSUPPORTED;
-    *bytes = m ? align_up(panel_bytes(rows, cols)) + align_up(panel_bytes(m, rows)) +
-                     align_up(mm_transposed_partial(rows, cols, 1, m))
-               : 0;
+    *bytes = m ? align_up(2 * rows * cols) + align_up(mm_transposed_partial(rows, cols, 1, m)) : 0;
     return AFX_OK;
 }
 
@@ -345,14 +353,12 @@ int afx_restore_gemm_t_async(const afx_info *info, const void *blob_dev, uint64_
     const Span out[] = {span(y_dev, m, cols, cols, 4), {ws_dev, need}};
     if (any_overlap(in, 2, out, 2) || pairs_overlap(out, 2)) return AFX_E_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const uint64_t at_a = align_up(panel_bytes(rows, cols)), at_partial = at_a + align_up(panel_bytes(m, rows));
-    const PanelJob job{info, blob_dev, rows, cols, u16_at(ws_dev, 0)};
-    rc = launch_restore_panels(&job, 1, s);
-    if (rc != AFX_OK) return rc;
-    rc = launch_pack_panels(d_dev, rows, m, rows, u16_at(ws_dev, at_a), s);
+    const afx_job job{info, blob_dev, ws_dev, 2 * rows * cols};
+    rc = afx_decode_layer_async(&job, 1, s);
     if (rc != AFX_OK) return rc;
     MmTransposed p{};
-    p.a[0] = u16_at(ws_dev, at_a);
+    p.a[0] = d_dev;
+    p.lda = rows;
     p.m = m;
     p.w[0] = u16_at(ws_dev, 0);
     p.n_mats = 1;
@@ -361,7 +367,7 @@ int afx_restore_gemm_t_async(const afx_info *info, const void *blob_dev, uint64_
     p.y32 = y_dev;
     p.ldy = cols;
     p.add = add != 0;
-    p.partial = reinterpret_cast<float *>(u16_at(ws_dev, at_partial));
+    p.partial = reinterpret_cast<float *>(u16_at(ws_dev, align_up(2 * rows * cols)));
     return launch_mm_transposed(p, s);
 }
 

@@ -1,6 +1,6 @@
 // afx_mm.h -- the product of BF16 activations with restored BF16 weights on
 // the matrix cores (afx_mm.hip), as the gated feed-forward block and the
-// transposed product use it. Both come as panels (afx_panels.h). Not installed.
+// transposed product use it. Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,9 +27,11 @@ struct MmGated {
 
 // y = a[0] w[0] (+ a[1] w[1]).
 struct MmTransposed {
-    const uint16_t *a[2];    // panels of BF16 [m, rows]
+    const uint16_t *a[2];    // BF16 [m, rows], row stride lda, 16-byte aligned rows; rows up to the next
+                             // multiple of 8 are read and must be 0
+    uint64_t lda;
     uint32_t m;
-    const uint16_t *w[2];    // panels of BF16 [rows, cols]
+    const uint16_t *w[2];    // BF16 [rows, cols], restored
     uint32_t n_mats;
     uint64_t rows, cols;
     float *y32;              // FP32 [m, cols], row stride ldy (one of y32, y16)

@@ -20,11 +20,16 @@
 //   * rows of 64 k (128 bytes): 16-byte chunk c of row r sits at chunk c ^
 //     ((r >> 1) & 7), so that the 16 rows a 16-lane phase reads cover all 64
 //     banks once;
-//   * transposed weights, 4 panels of 64 rows of 64 columns (128 bytes):
-//     32-byte unit q of row k sits at unit q ^ ((k & 2) | (k >> 3 & 1)); the
-//     operand's 8 consecutive k of one column come from two
-//     ds_read_b64_tr_b16 (a 16-lane group reads 4 rows of 16 columns and gets
-//     them transposed).
+//   * transposed weights, rows of 256 columns (512 bytes): 32-byte unit q of
+//     row k sits at unit q ^ ((k & 3) | (k >> 1 & 4)); the operand's 8
+//     consecutive k of one column come from two ds_read_b64_tr_b16 (a 16-lane
+//     group reads 4 rows of 16 columns and gets them transposed).
+//
+// The gated product reads 128 bytes of each of 256 rows, so its operands come
+// as panels (afx_panels.h: at 64 tokens and 17408 x 5112 weights 97 us, 142
+// from row-major ones); the transposed product reads 512 bytes of each of 64
+// weight rows and takes row-major weights (1024 tokens: 353 us, 370 from
+// panels) and tokens as they are.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -58,10 +63,11 @@ struct MmPlan {
 };
 
 struct MmArgs {
-    const uint16_t *a0, *a1;  // tokens' panels, of each matrix
-    const uint16_t *w0, *w1;  // weights' panels
+    const uint16_t *a0, *a1;  // gated: a0 tokens' panels; transposed: tokens of each matrix [m, ak], row stride lda
+    const uint16_t *w0, *w1;  // gated: panels; transposed: row-major, n columns
+    uint64_t lda;
     uint32_t m, n;            // tokens; outputs per token
-    uint32_t rows, panels;    // weight rows; panels of a weight matrix
+    uint32_t rows, ak;        // weight rows; transposed: steps held by a row of a0
     uint32_t k_tiles0;        // k-tiles of the first matrix
     uint32_t k_tiles;         // k-tiles of all matrices
     MmPlan plan;
@@ -172,48 +178,50 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
     const uint32_t kt_hi = (uint32_t)((uint64_t)p.k_tiles * (split + 1) / splits);
 
     // ---- what this lane loads -------------------------------------------
-    // Every buffer resource ends where its panel does (or further rows of it
-    // do): a load past that end puts zeros into LDS. So tokens past the last
-    // panel's last, weight rows past the last and reduction steps past the
-    // last come as zeros. (Other tokens past the last may be the next panel's;
-    // their outputs are not stored.)
-    // Instruction i of a wave covers rows 64 i + 8 wave + lane / 8 of 128
-    // bytes (transposed weights: rows 8 wave + lane / 8 of panel i).
+    // Every buffer resource ends where its rows do: a load past that end puts
+    // zeros into LDS. So tokens, weight rows and reduction steps (given an
+    // offset past every end) past the last come as zeros, whatever memory
+    // holds there. (Columns past the last of a transposed tile are the next
+    // row's; their outputs are not stored.)
+    constexpr uint32_t kPastEnd = 0x80000000u;
+    // Instruction i of a wave covers rows 64 i + 8 wave + lane / 8 of 64 steps.
     const uint32_t lr = 8 * wave + (lane >> 3);
-    const uint32_t off = 128 * lr + 16 * ((lane & 7) ^ ((lr >> 1) & 7));  // 64 i leaves the swizzle unchanged
-    const uint32_t a_end = (uint32_t)((p.m - m0) * 128);
-    uint32_t w_off = off, w_end = 0;
+    const uint32_t lc = (lane & 7) ^ ((lr >> 1) & 7);  // 64 i leaves the swizzle unchanged
+    const uint32_t a_row = kNN ? (uint32_t)(p.lda * 2) : 128u;  // bytes from row to row
+    const uint32_t a_off = a_row * lr + 16 * lc;
+    const uint32_t a_end = kNN ? (uint32_t)(((min((uint32_t)BM, p.m - m0) - 1) * p.lda + p.ak) * 2) : (p.m - m0) * 128;
+    uint32_t w_off, w_end = 0;
     if constexpr (!kNN) {
         // LDS row 64 i + 8 wave + ..: 32 rows of gate (waves 0-3), then 32 of up
-        w_off = 128 * (8 * (wave & 3) + (lane >> 3)) + 16 * ((lane & 7) ^ ((lr >> 1) & 7));
+        w_off = 128 * (8 * (wave & 3) + (lane >> 3)) + 16 * lc;
         w_end = (p.n - n0) * 128;
     } else {
-        // 32-byte unit (lane & 7) / 2 of row lr takes another unit's place
-        const uint32_t sw = (lr & 2) | ((lr >> 3) & 1);
-        w_off = 128 * lr + 32 * (((lane & 7) >> 1) ^ sw) + 16 * (lane & 1);
+        // rows of 256 columns: instruction i covers rows 16 i + 2 wave + lane / 32
+        const uint32_t wk_row = 2 * wave + (lane >> 5);
+        const uint32_t sw = (wk_row & 3) | ((wk_row >> 1) & 4);
+        w_off = wk_row * (2 * p.n) + 32 * (((lane & 31) >> 1) ^ sw) + 16 * (lane & 1);
     }
 
     // Request k-tile kt into a buffer.
     auto stage = [&](uint32_t kt, uint8_t *tok, uint8_t *wt) {
         const bool second = kNN && kt >= p.k_tiles0;
-        const uint32_t panel = kt - (second ? p.k_tiles0 : 0u);
+        const uint32_t kl = kt - (second ? p.k_tiles0 : 0u), k0 = kl * kBK;  // within the matrix
         uint8_t *tok_w = tok + wave * 1024, *wt_w = wt + wave * 1024;
-        const auto ra = buffer((second ? p.a1 : p.a0) + ((uint64_t)panel * p.m + m0) * kBK, a_end);
+        const auto ra = kNN ? buffer((second ? p.a1 : p.a0) + m0 * p.lda, a_end)
+                            : buffer(p.a0 + ((uint64_t)kl * p.m + m0) * kBK, a_end);
+        // (transposed: steps come in whole chunks of 8)
+        const uint32_t a_step = kNN ? 2 * k0 + (k0 + 8 * lc < p.ak ? 0u : kPastEnd) : 0u;
 #pragma unroll
-        for (int i = 0; i < kTokInstr; ++i) load_to_lds(ra, off + i * 8192, tok_w + i * 8192);
+        for (int i = 0; i < kTokInstr; ++i) load_to_lds(ra, a_off + 64 * i * a_row + a_step, tok_w + i * 8192);
         if constexpr (!kNN) {
-            const auto rw = buffer((wave < 4 ? p.w0 : p.w1) + ((uint64_t)panel * p.rows + n0) * kBK, w_end);
+            const auto rw = buffer((wave < 4 ? p.w0 : p.w1) + ((uint64_t)kl * p.rows + n0) * kBK, w_end);
 #pragma unroll
             for (int i = 0; i < 4; ++i) load_to_lds(rw, w_off + i * 4096, wt_w + i * 8192);
         } else {
-            const uint16_t *w = second ? p.w1 : p.w0;
+            const auto rw = buffer((second ? p.w1 : p.w0) + (uint64_t)k0 * p.n + n0,
+                                   (uint32_t)(((min(kBK, p.rows - k0) - 1) * (uint64_t)p.n + (p.n - n0)) * 2));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t col = n0 / kBK + i;  // the panel of these columns
-                const auto rw = buffer(w + ((uint64_t)min(col, p.panels - 1) * p.rows + panel * kBK) * kBK,
-                                       col < p.panels ? (p.rows - panel * kBK) * 128 : 0u);
-                load_to_lds(rw, w_off, wt_w + i * 8192);
-            }
+            for (int i = 0; i < 4; ++i) load_to_lds(rw, w_off + i * 32 * p.n, wt_w + i * 8192);
         }
     };
 
@@ -230,20 +238,20 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
         const uint32_t row = row0 + fr, c = (2 * ks + half) ^ ((row >> 1) & 7);
         return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(tile + row * 128 + 16 * c));
     };
-    // The same of columns l mod 32 and 32 + l mod 32 of the wave's panel of a
+    // The same of columns l mod 32 and 32 + l mod 32 of the wave's 64 of a
     // transposed tile. (The four reads and their wait are one block: through
     // the compiler's builtin, every transposing read would wait for all loads
     // into LDS, whichever buffer they fill.)
     auto frags_t = [&](uint8_t *tile, uint32_t ks, bf16x8 (&f)[2]) {
         const uint32_t k = 16 * ks + 8 * half + ((lane & 15) >> 2);
-        const uint32_t unit = (lane >> 4) & 1, sw = (k & 2) | ((k >> 3) & 1);
-        const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)tile + wn * 8192 +
-                            k * 128 + 8 * (lane & 3);
+        const uint32_t unit = 4 * wn + ((lane >> 4) & 1), sw = (k & 3) | ((k >> 1) & 4);
+        const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)tile + k * 512 +
+                            8 * (lane & 3);
         s16x4 v0, v1, v2, v3;
         asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
-                     "ds_read_b64_tr_b16 %1, %4 offset:512\n\t"
+                     "ds_read_b64_tr_b16 %1, %4 offset:2048\n\t"
                      "ds_read_b64_tr_b16 %2, %5\n\t"
-                     "ds_read_b64_tr_b16 %3, %5 offset:512\n\t"
+                     "ds_read_b64_tr_b16 %3, %5 offset:2048\n\t"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3)
                      : "v"(at + 32 * (unit ^ sw)), "v"(at + 32 * ((unit + 2) ^ sw))
@@ -442,7 +450,7 @@ int launch_mm_gated(const MmGated &q, hipStream_t stream) {
     p.w1 = q.wu;
     p.m = q.m;
     p.n = p.rows = (uint32_t)q.rows;
-    p.k_tiles0 = p.k_tiles = p.panels = (uint32_t)panel_count(q.cols);
+    p.k_tiles0 = p.k_tiles = (uint32_t)panel_count(q.cols);
     p.plan = gated_plan(q.rows, q.cols, q.m);
     p.partial = q.partial;
     p.h = q.h;
@@ -466,7 +474,8 @@ int launch_mm_transposed(const MmTransposed &q, hipStream_t stream) {
     p.m = q.m;
     p.n = (uint32_t)q.cols;
     p.rows = (uint32_t)q.rows;
-    p.panels = (uint32_t)panel_count(q.cols);
+    p.lda = q.lda;
+    p.ak = (uint32_t)((q.rows + 7) / 8 * 8);
     p.k_tiles0 = (uint32_t)panel_count(q.rows);
     p.k_tiles = p.k_tiles0 * q.n_mats;
     p.plan = transposed_plan(q.rows, q.cols, q.n_mats, q.m);
