@@ -18,7 +18,8 @@ tensor-1024 (1024x1024), q_proj (5120x5120), embedding (151936x5120), disk
 (the whole model stored compressed in a file, read cold, copied and
 restored), tiers (the model spread over residency tiers under memory
 budgets), gemv and gemm (the restore fused into the products of one layer's
-matrices) and token (one token's products over the whole model).
+matrices), token (one token's products over the whole model) and ffn (the
+feed-forward half of one layer over coded weights, forward and backward).
 
 Prints one JSON line with the throughput of restored BF16, the HBM roofline
 fraction of the decode kernel (hipEvent timing on the launch stream), and the
@@ -132,10 +133,10 @@ def main() -> int:
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--workload", default="model",
                     choices=["layer", "tensor-1024", "q_proj", "embedding", "model", "disk", "tiers", "gemv", "gemm",
-                             "token"])
+                             "token", "ffn"])
     ap.add_argument("--m", type=int, default=None,
                     help="tokens (activation rows) of the fused products: 1, 2 or 4 for --workload gemv "
-                         "(default 1), any for --workload gemm (default 64)")
+                         "(default 1), any for --workload gemm (default 64) and ffn (default 1024)")
     ap.add_argument("--layers", type=int, default=40,
                     help="decoder layers of the whole model (--workload model or disk)")
     ap.add_argument("--store-dir", default=os.environ.get("TMPDIR") or "/tmp",
@@ -178,6 +179,8 @@ def main() -> int:
         return bench_gemv(args, threads)
     if args.workload == "token":
         return bench_token(args, threads)
+    if args.workload == "ffn":
+        return bench_ffn(args, threads)
     workload, specs = workload_specs(args.workload)
     if args.max_workgroups < 0:
         print("--max-workgroups must be positive", file=sys.stderr)
@@ -658,6 +661,93 @@ def bench_token(args, threads: int) -> int:
         "cpu_baseline": None,
     }
     print(json.dumps(line), flush=True)
+    return 0 if within else 1
+
+
+def bench_ffn(args, threads: int) -> int:
+    """The feed-forward half of one decoder layer over coded weights: a step
+    is the norm, gated block, down product, residual add and next norm of m
+    tokens and then their gradients (ffn.FeedForward). Compared with the same
+    step in torch on the BF16 weights already restored, and on weights
+    restored in the step (once forward, once backward: a layer's weights are
+    not kept between the two)."""
+    import torch
+
+    from lossless_bf16_weight_afx_amd import afx, ffn, synth
+
+    dev = torch.device("cuda:0")
+    m = args.m if args.m is not None else 1024
+    if m < 1:
+        raise SystemExit("--m must be at least 1")
+    specs = [sp for sp in synth.decoder_layer(0) if sp.name.split(".")[-1].split("_")[0] in ("gate", "up", "down")]
+    mats, wbf = [], []
+    for sp in specs:
+        blob = afx.afx_encode(synth.generate(sp, threads=threads), sp.shape, threads=threads)
+        mats.append((afx.afx_query(blob), torch.from_numpy(blob).to(dev)))
+        wbf.append(torch.empty(sp.shape, dtype=torch.bfloat16, device=dev))
+    restore = afx.make_jobs([(i, b.data_ptr(), w.data_ptr(), 2 * w.numel()) for (i, b), w in zip(mats, wbf)])
+    stream = torch.cuda.current_stream(dev)
+    afx.afx_decode_layer_async(restore, stream.cuda_stream)
+    (width, d), n_total = specs[0].shape, sum(w.numel() for w in wbf)
+    gen = torch.Generator(device="cpu").manual_seed(13)
+    new = lambda *shape: torch.randn(shape, generator=gen).to(torch.bfloat16).to(dev)  # noqa: E731
+    r, dro, dxo = new(m, d), new(m, d), new(m, d)
+    w_pre, w_next = 1 + 0.1 * new(d), 1 + 0.1 * new(d)
+    block = ffn.FeedForward(*mats, d, width, w_pre, w_next=w_next, max_tokens=m, training=True)
+
+    def fused(k):
+        block.forward(r)
+        return block.backward(r, dro, dxo)
+
+    def forward(k):
+        return block.forward(r)
+
+    leaf, wp, wn = (t.clone().requires_grad_() for t in (r, w_pre, w_next))
+
+    def torch_forward():
+        rms = lambda t, w: torch.nn.functional.rms_norm(t, (d,), w, 1e-6)  # noqa: E731
+        xn = rms(leaf, wp)
+        h = torch.nn.functional.silu(xn @ wbf[0].t()) * (xn @ wbf[1].t())
+        ro = leaf + h @ wbf[2].t()
+        return ro, rms(ro, wn)
+
+    def torch_step(k):
+        leaf.grad = wp.grad = wn.grad = None
+        torch.autograd.backward(torch_forward(), (dro, dxo))
+
+    def restore_step(k):
+        leaf.grad = wp.grad = wn.grad = None
+        afx.afx_decode_layer_async(restore, stream.cuda_stream)
+        out = torch_forward()
+        afx.afx_decode_layer_async(restore, stream.cuda_stream)
+        torch.autograd.backward(out, (dro, dxo))
+
+    # check (outside the timing): within the BF16 roundings of both sides
+    got = [t.clone() for t in (fused(0), block.r_out, block.xn_next)]
+    torch_step(0)
+    with torch.no_grad():
+        ro, xo = torch_forward()
+    torch.cuda.synchronize()
+    errors = [float((a.float() - b.float()).norm() / b.float().norm()) for a, b in zip(got, (leaf.grad, ro, xo))]
+    within = all(e <= 20 * 2.0 ** -8 for e in errors)
+    ms = _time_steps(stream, fused, args.steps, args.warmup)
+    ms_fwd = _time_steps(stream, forward, args.steps, args.warmup)
+    ms_torch = _time_steps(stream, torch_step, args.steps, args.warmup)
+    ms_restore = _time_steps(stream, restore_step, args.steps, args.warmup)
+    flop = 4 * m * n_total  # forward, and the same backward (weights are constants)
+    print(json.dumps({
+        "metric": "feed-forward half of a layer over coded weights, forward and backward, on 1 MI355X",
+        "value": round(m / (ms * 1e-3), 1), "unit": "tokens/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(ms, 5), "higher_is_better": True, "scaling": "weak",
+        "vs_baseline": None, "dtype": "bf16 products, f32 sums", "data": "synthetic",
+        "config": {"workload": f"qwen3-14b-feed-forward-m{m}", "matrices": len(specs), "weights": n_total, "m": m,
+                   "blob_bytes": sum(int(i.blob_bytes) for i, _ in mats)},
+        "within_bound": bool(within), "tflops": round(flop / (ms * 1e-3) / 1e12, 1),
+        "compare": {"unit": "us", "step": round(ms * 1e3, 1), "forward": round(ms_fwd * 1e3, 1),
+                    "torch_step_on_restored": round(ms_torch * 1e3, 1),
+                    "torch_step_restoring_twice": round(ms_restore * 1e3, 1)},
+        "cpu_baseline": None,
+    }), flush=True)
     return 0 if within else 1
 
 

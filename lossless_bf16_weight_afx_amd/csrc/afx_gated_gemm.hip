@@ -133,6 +133,8 @@ __device__ inline Words seg_words_of(const Bits &b) {
     return w;
 }
 static_assert(kSegMaxStart < 1u << 16, "a start fits 16 bits");
+static_assert(chain_word(32 * kSegRev + kLead) + 1 < kSegRow, "a chain's first words are in the slice");
+static_assert(chain_word(32 * kSegRev + kLead - kSegMaxStart - 32 * kMaxLen) >= 1, "and its last, read ahead");
 
 // The counters of the chains of the lane's groups q and q + 4 of row l mod 16.
 __device__ inline void chain_starts(uint32_t starts, uint32_t lane, uint32_t &r1, uint32_t &r2) {
