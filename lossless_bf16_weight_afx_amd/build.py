@@ -16,9 +16,9 @@ SOURCES = [os.path.join(CSRC, "afx_host.cpp"), os.path.join(CSRC, "afx_io.cpp"),
            os.path.join(CSRC, "afx_host_decode.cpp"), os.path.join(CSRC, "afx_decode.hip"),
            os.path.join(CSRC, "afx_gemv.hip"), os.path.join(CSRC, "afx_gemm.hip"),
            os.path.join(CSRC, "afx_gated.hip"), os.path.join(CSRC, "afx_gated_gemv.hip"),
-           os.path.join(CSRC, "afx_gated_gemm.hip"),
+           os.path.join(CSRC, "afx_gated_gemm.hip"), os.path.join(CSRC, "afx_gemm_t.hip"),
            os.path.join(CSRC, "afx_mm.hip"), os.path.join(CSRC, "afx_panels.hip"),
-            os.path.join(CSRC, "afx_norm.hip")]
+           os.path.join(CSRC, "afx_norm.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-FP32 instructions are kept out of every device build.

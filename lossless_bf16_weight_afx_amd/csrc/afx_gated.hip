@@ -18,6 +18,7 @@
 #include "afx_act.h"
 #include "afx_gated_gemm.h"
 #include "afx_gated_gemv.h"
+#include "afx_gemm_t.h"
 #include "afx_mm.h"
 
 namespace afx {
@@ -152,6 +153,13 @@ GatedPath gated_path(uint64_t cols, uint32_t m) {
     return m <= kGatedGemmTokens && cols % kGroup == 0 ? kPathGemm : kPathRestore;
 }
 
+// Whether a transposed product takes the coded matrices as they are, or has
+// them restored to the workspace first (the gradient of two 17408 x 5120
+// matrices, fused and restored: 16 tokens 107 and 211 us, 64 138 and 215;
+// 5120 x 17408, 64 tokens: 78 and 110. Above 64 the fused kernel's sums would
+// not fit its registers.)
+bool transposed_fused(uint64_t cols, uint32_t m) { return m <= kGemmTTokens && cols % kGroup == 0; }
+
 // Where the pieces of a gated call's workspace lie, and its size.
 struct GatedSpace {
     uint64_t wg, wu, a0, a1, partial, bytes;  // a0: x as panels; or dg, and a1: du
@@ -165,14 +173,17 @@ GatedSpace gated_space(uint64_t rows, uint64_t cols, uint32_t m, bool backward) 
         s.bytes = path == kPathGemv ? gated_gemv_space(rows, cols, m) : gated_gemm_space(rows, cols, m);
         return s;
     }
-    const uint64_t w = align_up(backward ? 2 * rows * cols : panel_bytes(rows, cols));
+    const bool fused = backward && transposed_fused(cols, m);
+    const uint64_t w = fused ? 0 : align_up(backward ? 2 * rows * cols : panel_bytes(rows, cols));
     const uint64_t a = align_up(backward ? 2 * m * pad8(rows) : panel_bytes(m, cols));
     s.wu = w;
     s.a0 = 2 * w;
     s.a1 = s.a0 + (backward ? a : 0);
     s.partial = s.a1 + a;
     s.bytes = s.partial +
-              align_up(backward ? mm_transposed_partial(rows, cols, 2, m) : mm_gated_partial(rows, cols, m));
+              align_up(fused      ? gemm_t_space(rows, cols, 2, m)
+                       : backward ? mm_transposed_partial(rows, cols, 2, m)
+                                  : mm_gated_partial(rows, cols, m));
     return s;
 }
 
@@ -307,15 +318,20 @@ int afx_restore_gated_backward_async(const afx_gated *w, uint32_t m, const float
             !misaligned(u_dev, 8) && !misaligned(dg_dev, 8) && !misaligned(du_dev, 8);
     rc = launch_grad(a, w->act, s);
     if (rc != AFX_OK) return rc;
+    const uint16_t *dg = direct ? dg_dev : a.wdg, *du = direct ? du_dev : a.wdu;
+    const uint64_t lda = direct ? gu_stride : a.padded;
+    if (transposed_fused(w->cols, m))
+        return launch_gemm_t({{w->gate_info, w->up_info}, {w->gate_blob_dev, w->up_blob_dev}, 2, w->rows, w->cols,
+                              {dg, du}, lda, m, nullptr, dx_dev, dx_stride, false}, ws + sp.partial, s);
     const size_t bytes = 2 * w->rows * w->cols;
     const afx_job jobs[2] = {{w->gate_info, w->gate_blob_dev, u16_at(ws, sp.wg), bytes},
                              {w->up_info, w->up_blob_dev, u16_at(ws, sp.wu), bytes}};
     rc = afx_decode_layer_async(jobs, 2, s);
     if (rc != AFX_OK) return rc;
     MmTransposed p{};
-    p.a[0] = direct ? dg_dev : a.wdg;
-    p.a[1] = direct ? du_dev : a.wdu;
-    p.lda = direct ? gu_stride : a.padded;
+    p.a[0] = dg;
+    p.a[1] = du;
+    p.lda = lda;
     p.m = m;
     p.w[0] = u16_at(ws, sp.wg);
     p.w[1] = u16_at(ws, sp.wu);
@@ -333,7 +349,10 @@ int afx_restore_gemm_t_workspace(uint64_t rows, uint64_t cols, uint32_t m, size_
     const int rc = check_sizes(rows, cols, m);
     if (rc != AFX_OK) return rc;
     if (rows % 8) return AFX_E_UNSUPPORTED;
-    *bytes = m ? align_up(2 * rows * cols) + align_up(mm_transposed_partial(rows, cols, 1, m)) : 0;
+    *bytes = m == 0                     ? 0
+             : transposed_fused(cols, m) ? align_up(gemm_t_space(rows, cols, 1, m))
+                                         : align_up(2 * rows * cols) +
+                                               align_up(mm_transposed_partial(rows, cols, 1, m));
     return AFX_OK;
 }
 
@@ -353,6 +372,9 @@ int afx_restore_gemm_t_async(const afx_info *info, const void *blob_dev, uint64_
     const Span out[] = {span(y_dev, m, cols, cols, 4), {ws_dev, need}};
     if (any_overlap(in, 2, out, 2) || pairs_overlap(out, 2)) return AFX_E_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (transposed_fused(cols, m))
+        return launch_gemm_t({{info, nullptr}, {blob_dev, nullptr}, 1, rows, cols, {d_dev, nullptr}, rows, m, y_dev,
+                              nullptr, cols, add != 0}, static_cast<uint8_t *>(ws_dev), s);
     const afx_job job{info, blob_dev, ws_dev, 2 * rows * cols};
     rc = afx_decode_layer_async(&job, 1, s);
     if (rc != AFX_OK) return rc;

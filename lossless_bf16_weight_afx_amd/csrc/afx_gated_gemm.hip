@@ -27,7 +27,7 @@
 
 #include "afx_act.h"
 #include "afx_gated_gemm.h"
-#include "afx_slab.h"
+#include "afx_segments.h"
 
 namespace afx {
 namespace {
@@ -60,81 +60,6 @@ __global__ __launch_bounds__(256) void afx_gated_pack_kernel(const uint16_t *x, 
     if (t < m && col < cols) v = *reinterpret_cast<const uint4 *>(x + t * ldx + col);
     *reinterpret_cast<uint4 *>(out + ((uint64_t)o * kWave + lane) * 8) = v;
 }
-
-// A tile's place in its tensor: bases of its first element, so that a lane's
-// own offsets stay 32-bit.
-struct Tile {
-    const uint64_t *base;   // chunk_base of the tile's first chunk
-    const uint16_t *gap;    // gap of its first group
-    const uint8_t *sm;      // its first sign/mantissa byte
-    uint32_t in_chunk;      // its first element's place in that chunk
-    uint32_t left;          // elements from its first to the tensor's end (at most 2^31)
-    uint32_t chunks;        // chunk_base entries from `base` to the last one
-};
-__device__ inline Tile tile_at(const TensorDesc &T, uint32_t tile, uint32_t cols) {
-    const uint64_t e0 = (uint64_t)tile * kGatedWaveRows * cols;
-    return Tile{T.chunk_base + (e0 >> 12), T.gap + (e0 >> 5), T.signmant + e0, (uint32_t)e0 & (kChunk - 1),
-                (uint32_t)umin64(T.n - e0, 1u << 31), T.n_chunks - (uint32_t)(e0 >> 12)};
-}
-
-// Loads are in quads of lanes per row (lane l: row l / 4, part c = l mod 4),
-// so that a quad's accesses fall into one cache line; decoding and multiplying
-// are with row l mod 16 and q = l / 16. What the two orders hand over goes
-// through LDS.
-
-// A row's part of a slab: its elements [start, start + len), from the tile's
-// first element.
-struct Seg {
-    uint32_t start, len;
-};
-
-// What the bit offsets of the lane's groups 2 c and 2 c + 1 of a segment and
-// of its end are made of, kept as loaded and added up only where used. (A
-// segment lies in one chunk or ends in the next; a group past the row's end
-// repeats the row's last one: it is decoded, not used.)
-struct Bits {
-    u32x4 base;      // u64 bit bases of the chunk that the segment starts in, and of the next
-    uint32_t a, b, e;  // gaps of the lane's groups and of the group after the segment
-    uint32_t next_a, next_b, next_e;  // whether each is in the next chunk
-    uint32_t e_mask;   // 0 where the segment ends the tensor (the stream's end, with no gap)
-};
-__device__ inline Bits seg_bits(const Tile &t, const Seg &g, uint32_t c) {
-    Bits b;
-    const uint32_t ch = (t.in_chunk + g.start) >> 12, most = g.len / kGroup - 1, end = g.start + g.len;
-    const uint32_t ga = min(2 * c, most), gb = min(2 * c + 1, most);
-    __builtin_memcpy(&b.base, t.base + ch, 16);  // (8-byte aligned; the entry after the last chunk's exists)
-    const bool last = end >= t.left;
-    b.a = t.gap[(g.start >> 5) + ga];
-    b.b = t.gap[(g.start >> 5) + gb];
-    b.e = t.gap[last ? 0 : end >> 5];
-    b.next_a = (t.in_chunk + g.start + kGroup * ga) >> 12 != ch;
-    b.next_b = (t.in_chunk + g.start + kGroup * gb) >> 12 != ch;
-    b.next_e = last || (t.in_chunk + end) >> 12 != ch;
-    b.e_mask = last ? 0u : ~0u;
-    return b;
-}
-
-// A row segment's staged words [wa, wa + nw), and where the lane's groups
-// start in them, in bits (16 each). Differences of positions are taken modulo
-// 2^32: they are small, or, on a corrupt stream, clamped.
-struct Words {
-    uint64_t wa;
-    uint32_t nw, starts;
-};
-__device__ inline Words seg_words_of(const Bits &b) {
-    const uint64_t b0 = ((uint64_t)b.base.y << 32) | b.base.x, bn = ((uint64_t)b.base.w << 32) | b.base.z;
-    const uint64_t pa = (b.next_a ? bn : b0) + b.a;
-    Words w;
-    w.wa = seg_first_word(quad_first(pa));
-    const uint32_t first = (uint32_t)w.wa << 5;
-    w.nw = min((((b.next_e ? b.base.z : b.base.x) + (b.e & b.e_mask) - first + 31) >> 5) + 1, kSegWords);
-    w.starts = min((uint32_t)pa - first, kSegMaxStart) |
-               min((b.next_b ? b.base.z : b.base.x) + b.b - first, kSegMaxStart) << 16;
-    return w;
-}
-static_assert(kSegMaxStart < 1u << 16, "a start fits 16 bits");
-static_assert(chain_word(32 * kSegRev + kLead) + 1 < kSegRow, "a chain's first words are in the slice");
-static_assert(chain_word(32 * kSegRev + kLead - kSegMaxStart - 32 * kMaxLen) >= 1, "and its last, read ahead");
 
 // The counters of the chains of the lane's groups q and q + 4 of row l mod 16.
 __device__ inline void chain_starts(uint32_t starts, uint32_t lane, uint32_t &r1, uint32_t &r2) {
@@ -203,6 +128,7 @@ void afx_gated_gemm_kernel(const SlabArgs p) {
     // The wave's 16 rows of tile t, and the lane's part of a slab. Rows past
     // the matrix repeat its last ones; their sums are not used.
     auto rows_of = [&](uint32_t t) { return min(t * p.split.waves + wave, p.split.row_tiles - 1); };
+    auto tile_of = [&](uint32_t t) { return tile_at(T, (uint64_t)rows_of(t) * kGatedWaveRows * p.cols); };
     auto segment = [&](uint32_t t, uint32_t k) {
         return Seg{umin32(lrow, p.rows - 1 - rows_of(t) * kGatedWaveRows) * p.cols + k, umin32(kSlabCols, p.cols - k)};
     };
@@ -219,7 +145,7 @@ void afx_gated_gemm_kernel(const SlabArgs p) {
     Bits bits;
     u32x4 w0, w1, sm[4];  // the lane's 8 of the row's first 32 words; 4 of 16 times 16 sign/mantissa bytes
     auto load_bits = [&](uint32_t t, uint32_t k) {
-        bits = seg_bits(tile_at(T, rows_of(t), p.cols), segment(t, k), c);
+        bits = seg_bits(tile_of(t), segment(t, k), c);
     };
     auto load_words = [&] {
         w0 = __builtin_bit_cast(u32x4, load_words4(T, words.wa + 4 * c));
@@ -227,14 +153,14 @@ void afx_gated_gemm_kernel(const SlabArgs p) {
     };
     auto load_sm = [&](uint32_t t, uint32_t k) {  // read once: not kept in the caches
         const Seg g = segment(t, k);
-        const uint8_t *row = tile_at(T, rows_of(t), p.cols).sm;
+        const uint8_t *row = tile_of(t).sm;
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i)
             sm[i] = __builtin_nontemporal_load(
                 reinterpret_cast<const u32x4 *>(row + g.start + min(64 * i + 16 * c, g.len - 16)));
     };
     load_bits(tile, k0);
-    words = seg_words_of(bits);
+    words = seg_words_of<4, kSegWords, kSegMaxStart>(bits);
     load_words();
     load_bits(tile_n, k0_n);
     [[clang::always_inline]] build_lut<kWavesWG * kWave, true>(len, lds.plut, lds.scratch);
@@ -266,7 +192,7 @@ void afx_gated_gemm_kernel(const SlabArgs p) {
         // sign/mantissa bytes, the next slab's words, the one after's offsets.
         load_sm(tile, k0);
         if (s + 1 < s1) {
-            words = seg_words_of(bits);
+            words = seg_words_of<4, kSegWords, kSegMaxStart>(bits);
             load_words();
         }
         if (s + 2 < s1) {
@@ -370,21 +296,6 @@ __global__ __launch_bounds__(256) void afx_gated_gemm_join_kernel(const SlabArgs
         q.g[(uint64_t)t * q.ldgu + f] = __builtin_bit_cast(uint16_t, (__bf16)g);
         q.u[(uint64_t)t * q.ldgu + f] = __builtin_bit_cast(uint16_t, (__bf16)u);
     }
-}
-
-TensorDesc tensor(const afx_info *info, const void *blob) {
-    const uint8_t *b = static_cast<const uint8_t *>(blob);
-    TensorDesc t{};
-    t.code_len = b + info->off_code_len;
-    t.chunk_base = reinterpret_cast<const uint64_t *>(b + info->off_chunk_base);
-    t.gap = reinterpret_cast<const uint16_t *>(b + info->off_gap);
-    t.signmant = b + info->off_signmant;
-    t.exp = reinterpret_cast<const uint32_t *>(b + info->off_exp);
-    t.n = info->n_elems;
-    t.exp_words = info->exp_words;
-    t.last_word4 = last_word4(info->exp_words);
-    t.n_chunks = (uint32_t)info->n_chunks;
-    return t;
 }
 
 uint64_t align_up(uint64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }

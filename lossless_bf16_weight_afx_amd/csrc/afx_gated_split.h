@@ -33,7 +33,18 @@ constexpr uint32_t range_of(const GatedSplit &s, uint32_t i) {
     return (uint32_t)((((uint64_t)i + 1) * s.ranges + total - 1) / total - 1);
 }
 
-// At most `resident` ranges, none empty. A small matrix is given to fewer
+// s's slabs in at most `resident` ranges, none empty.
+constexpr GatedSplit with_ranges(GatedSplit s, uint32_t resident) {
+    const uint64_t total = (uint64_t)s.tiles * s.tile_slabs;
+    s.ranges = (uint32_t)(total < resident ? total : resident);
+    // a tile's slabs reach over at most this many ranges of total / ranges or more
+    const uint32_t least = (uint32_t)(total / s.ranges);
+    s.most = (s.tile_slabs - 1) / least + 2;
+    if (s.most > s.tile_slabs) s.most = s.tile_slabs;
+    return s;
+}
+
+// Both for the tiles of one matrix. A small matrix is given to fewer
 // waves of each workgroup, so that there are slabs for all workgroups. rows <
 // 2^21 and cols < 2^22 keep the slab count below 2^32.
 constexpr GatedSplit split_slabs(uint64_t rows, uint64_t cols, uint32_t resident, uint32_t waves) {
@@ -44,13 +55,7 @@ constexpr GatedSplit split_slabs(uint64_t rows, uint64_t cols, uint32_t resident
         s.tiles = (s.row_tiles + s.waves - 1) / s.waves;
         if (s.waves == 1 || (uint64_t)s.tiles * s.tile_slabs >= resident) break;
     }
-    const uint64_t total = (uint64_t)s.tiles * s.tile_slabs;
-    s.ranges = (uint32_t)(total < resident ? total : resident);
-    // a tile's slabs reach over at most this many ranges of total / ranges or more
-    const uint32_t least = (uint32_t)(total / s.ranges);
-    s.most = (s.tile_slabs - 1) / least + 2;
-    if (s.most > s.tile_slabs) s.most = s.tile_slabs;
-    return s;
+    return with_ranges(s, resident);
 }
 
 // Where the sums of one wave's rows from one range go: tile, the range's place
