@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "afx_internal.h"
 
@@ -59,43 +60,57 @@ struct Lanes {
     __device__ uint32_t at(int i, int e) const {
         return kVec ? 8 * (lane + (uint32_t)i * team) + (uint32_t)e : lane + (uint32_t)(8 * i + e) * team;
     }
-    template <class F>
-    __device__ void load(const float *p, F &&put) const {
+    // The lane's values of a row as loaded: from the row's first values where
+    // it has none of its own, so that no load waits behind a branch.
+    template <class T>
+    struct Raw {
+        static constexpr int kParts = kVec ? 8 * I * (int)sizeof(T) / 16 : 8 * I;
+        std::conditional_t<kVec, uint4, T> part[kParts];
+    };
+    template <class T>
+    __device__ Raw<T> fetch(const T *p) const {
+        Raw<T> raw;
+        constexpr int kEach = Raw<T>::kParts / I;  // parts of 8 values
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if constexpr (kVec) {
-                float4 a = make_float4(0, 0, 0, 0), b = a;
-                if (at(i, 0) < d) {
-                    a = *reinterpret_cast<const float4 *>(p + at(i, 0));
-                    b = *reinterpret_cast<const float4 *>(p + at(i, 0) + 4);
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                if constexpr (kVec) {
+                    const uint32_t c = at(i, 0) < d ? at(i, 0) : 0;
+                    raw.part[kEach * i + k] = reinterpret_cast<const uint4 *>(p + c)[k];
+                } else {
+                    raw.part[kEach * i + k] = p[at(i, k) < d ? at(i, k) : 0];
                 }
-                const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) put(8 * i + e, v[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) put(8 * i + e, at(i, e) < d ? p[at(i, e)] : 0.f);
             }
-        }
+        return raw;
     }
-    template <class F>
-    __device__ void load(const uint16_t *p, F &&put) const {
+    template <class T, class F>
+    __device__ void each(const Raw<T> &raw, F &&put) const {
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if constexpr (kVec) {
-                uint4 a = make_uint4(0, 0, 0, 0);
-                if (at(i, 0) < d) a = *reinterpret_cast<const uint4 *>(p + at(i, 0));
-                const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+        for (int i = 0; i < I; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    put(8 * i + 2 * e, bf16(v[e] & 0xFFFFu));
-                    put(8 * i + 2 * e + 1, __uint_as_float(v[e] & 0xFFFF0000u));
+            for (int e = 0; e < 8; ++e) {
+                float v;
+                if constexpr (!kVec) {
+                    if constexpr (sizeof(T) == 4)
+                        v = raw.part[8 * i + e];
+                    else
+                        v = bf16(raw.part[8 * i + e]);
+                } else {
+                    constexpr int kPer = 16 / (int)sizeof(T);  // values of a part
+                    const uint4 &q = raw.part[(8 * i + e) / kPer];
+                    const int w = e % kPer * (int)sizeof(T) / 4;
+                    const uint32_t u = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
+                    v = sizeof(T) == 4 ? __uint_as_float(u)
+                        : e % 2        ? __uint_as_float(u & 0xFFFF0000u)
+                                       : bf16(u & 0xFFFFu);
                 }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) put(8 * i + e, at(i, e) < d ? bf16(p[at(i, e)]) : 0.f);
+                put(8 * i + e, at(i, e) < d ? v : 0.f);
             }
-        }
+    }
+    template <class T, class F>
+    __device__ void load(const T *p, F &&put) const {
+        each(fetch(p), put);
     }
     template <class F>
     __device__ void store(float *p, F &&get) const {
@@ -202,30 +217,74 @@ __global__ __launch_bounds__(kTeam ? kTeamThreads : 1024) void afx_norm_kernel(c
 // Gradients. A workgroup goes through its rows with the sums over rows
 // (dw_pre, dw_post, a shared gate's dgate) in registers and writes them once,
 // for afx_norm_sum_kernel to add up in the order of the workgroups.
-template <uint32_t kTeam, bool kVec, int I, class R>
-__global__ __launch_bounds__(kTeam ? kTeamThreads : 1024) void afx_norm_grad_kernel(const NormArgs p) {
+//
+// For rows of up to 8192 values the next row is requested before this one is
+// worked on (registers: 28, or 32 for single values), and the vectors w_post,
+// w_pre and a shared gate are kept in LDS: read from memory in between, they
+// would wait for that row, loads being counted in order. (4096 rows of 5120,
+// FP32 stream: 109 us without, 126 with the request alone, 99 with both.)
+template <uint32_t kTeam, bool kVec, int I, class R, uint32_t kThreads>
+__global__ __launch_bounds__(kThreads) void afx_norm_grad_kernel(const NormArgs p) {
     __shared__ float sums[3][kMaxTeamWaves];
     constexpr int N = 8 * I;
+    constexpr bool kAhead = I == 1;
     const uint32_t team = kTeam ? kTeam : blockDim.x;
     const uint32_t teams = kTeam ? kTeamThreads / team : 1;
-    const Lanes<kTeam, kVec, I> L{threadIdx.x % team, team, p.d};
+    using Row = Lanes<kTeam, kVec, I>;
+    const Row L{threadIdx.x % team, team, p.d};
+    struct In {  // what a turn reads of its row
+        typename Row::template Raw<R> r, dr_out;
+        typename Row::template Raw<float> b;
+        typename Row::template Raw<uint16_t> dxn;
+    };
+    auto fetch = [&](uint64_t row0) {
+        const uint64_t row = row0 + threadIdx.x / team, rr = row < p.m ? row : 0;
+        In in;
+        in.r = L.fetch(static_cast<const R *>(p.r) + rr * p.r_stride);
+        if (p.b) in.b = L.fetch(p.b + rr * p.b_stride);
+        if (p.dr_out) in.dr_out = L.fetch(static_cast<const R *>(p.dr_out) + rr * p.dro_stride);
+        if (p.dxn) in.dxn = L.fetch(p.dxn + rr * p.dxn_stride);
+        return in;
+    };
+    const uint64_t step = (uint64_t)gridDim.x * teams;
+    uint64_t row0 = (uint64_t)blockIdx.x * teams;
+    In in, next;
+    const uint16_t *w_pre = p.w_pre, *w_post = p.w_post, *gate = p.gate;
+    if constexpr (kAhead) {
+        __shared__ __attribute__((aligned(16))) uint16_t vectors[3][kTeam ? 8 * kTeam : 8 * kThreads];
+        const uint16_t *from[3] = {p.w_pre, p.w_post, p.gate_stride ? nullptr : p.gate};
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (from[k])
+                for (uint32_t c = threadIdx.x; c < p.d; c += blockDim.x) vectors[k][c] = from[k][c];
+        if (row0 < p.m) next = fetch(row0);
+        __syncthreads();
+        w_pre = vectors[0];
+        w_post = vectors[1];
+        if (!p.gate_stride) gate = vectors[2];
+    }
     float dw_pre[N] = {}, dw_post[N] = {}, dgate[N] = {};
     // every lane takes every turn: the sums below are over whole waves
-    for (uint64_t row0 = (uint64_t)blockIdx.x * teams; row0 < p.m; row0 += (uint64_t)gridDim.x * teams) {
+    for (; row0 < p.m; row0 += step) {
         const uint64_t row = row0 + threadIdx.x / team;
         const bool ok = row < p.m;
-        const uint64_t rr = ok ? row : 0;
+        if constexpr (kAhead) {
+            in = next;
+            if (row0 + step < p.m) next = fetch(row0 + step);
+        } else {
+            in = fetch(row0);
+        }
         float v[N], dr[N], b[N];
         float s[3] = {0.f, 0.f, 0.f};  // r'^2, dxn w_pre r', b^2
 #pragma unroll
         for (int e = 0; e < N; ++e) dr[e] = b[e] = 0.f;
-        L.load(static_cast<const R *>(p.r) + rr * p.r_stride, [&](int e, float x) { v[e] = x; });
-        if (p.b) L.load(p.b + rr * p.b_stride, [&](int e, float x) { b[e] = x; });
-        if (p.dr_out) L.load(static_cast<const R *>(p.dr_out) + rr * p.dro_stride, [&](int e, float x) { dr[e] = x; });
+        L.each(in.r, [&](int e, float x) { v[e] = x; });
+        if (p.b) L.each(in.b, [&](int e, float x) { b[e] = x; });
+        if (p.dr_out) L.each(in.dr_out, [&](int e, float x) { dr[e] = x; });
         if (p.dxn) {
             float dn[N], dx[N];
-            L.load(p.dxn + rr * p.dxn_stride, [&](int e, float x) { dx[e] = x; });
-            L.load(p.w_pre, [&](int e, float x) { dn[e] = dx[e] * x; });
+            L.each(in.dxn, [&](int e, float x) { dx[e] = x; });
+            L.load(w_pre, [&](int e, float x) { dn[e] = dx[e] * x; });
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 s[0] = fmaf(v[e], v[e], s[0]);
@@ -257,14 +316,14 @@ __global__ __launch_bounds__(kTeam ? kTeamThreads : 1024) void afx_norm_grad_ker
             float bh[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) bh[e] = b[e] * k;
-            if (p.w_post) L.load(p.w_post, [&](int e, float x) { bh[e] *= x; });
+            if (p.w_post) L.load(w_post, [&](int e, float x) { bh[e] *= x; });
             if (p.dgate_rows) {
                 if (ok) L.store(p.dgate_rows + row * p.d, [&](int e) { return bh[e] * v[e]; });
             } else if (ok) {
 #pragma unroll
                 for (int e = 0; e < N; ++e) dgate[e] = fmaf(bh[e], v[e], dgate[e]);
             }
-            L.load(p.gate + rr * p.gate_stride, [&](int e, float x) { v[e] *= x; });
+            L.load(gate + (ok ? row : 0) * p.gate_stride, [&](int e, float x) { v[e] *= x; });
         }
         if (p.w_post) {
             float t[1] = {0.f};
@@ -272,7 +331,7 @@ __global__ __launch_bounds__(kTeam ? kTeamThreads : 1024) void afx_norm_grad_ker
 #pragma unroll
                 for (int e = 0; e < N; ++e) dw_post[e] = fmaf(v[e], b[e] * k, dw_post[e]);
             }
-            L.load(p.w_post, [&](int e, float x) { v[e] *= x; });
+            L.load(w_post, [&](int e, float x) { v[e] *= x; });
 #pragma unroll
             for (int e = 0; e < N; ++e) t[0] = fmaf(v[e], b[e], t[0]);
             team_sum<kTeam>(t, sums);
@@ -309,7 +368,7 @@ __global__ __launch_bounds__(kTeam ? kTeamThreads : 1024) void afx_norm_grad_ker
 
 // out[q] = sum over the workgroups' partial sums, in their order. 16 slices
 // of workgroups per column, then those in order.
-constexpr uint32_t kSumSlices = 16, kSumCols = 16;
+constexpr uint32_t kSumSlices = 32, kSumCols = 32;
 __global__ __launch_bounds__(kSumSlices *kSumCols) void afx_norm_sum_kernel(const float *part, uint32_t groups,
                                                                             uint32_t d, float *o0, float *o1,
                                                                             float *o2) {
@@ -318,8 +377,15 @@ __global__ __launch_bounds__(kSumSlices *kSumCols) void afx_norm_sum_kernel(cons
     float *o = q == 0 ? o0 : q == 1 ? o1 : o2;
     if (!o) return;
     float t = 0.f;
-    if (c < d)
-        for (uint32_t g = y; g < groups; g += kSumSlices) t += part[((uint64_t)g * 3 + q) * d + c];
+    const float *in = part + (uint64_t)q * d + min(c, d - 1);
+    constexpr uint32_t kAtOnce = 8;  // loads in flight; those past the last add 0
+    for (uint32_t g = y; g < groups; g += kAtOnce * kSumSlices) {
+        float v[kAtOnce];
+#pragma unroll
+        for (uint32_t k = 0; k < kAtOnce; ++k) v[k] = in[(uint64_t)min(g + k * kSumSlices, groups - 1) * 3 * d];
+#pragma unroll
+        for (uint32_t k = 0; k < kAtOnce; ++k) t += g + k * kSumSlices < groups ? v[k] : 0.f;
+    }
     s[y][threadIdx.x % kSumCols] = t;
     __syncthreads();
     if (y == 0 && c < d) {
@@ -342,22 +408,27 @@ NormShape norm_shape(uint64_t d) {
 uint32_t norm_blocks(const NormShape &s, uint32_t m, uint32_t most) {
     return (uint32_t)std::min<uint64_t>(((uint64_t)m + s.teams - 1) / s.teams, most);
 }
-constexpr uint32_t kForwardBlocks = 8192, kGradBlocks = 512;
+constexpr uint32_t kForwardBlocks = 8192;
+// Workgroups of the gradients' launch, each with its sums over its rows: one
+// or two on a CU.
+uint32_t grad_blocks(const NormShape &s, uint32_t m) { return norm_blocks(s, m, s.threads > 512 ? 256 : 512); }
 
-template <bool kGrad, uint32_t kTeam, bool kVec, int I>
+template <bool kGrad, uint32_t kTeam, bool kVec, int I, uint32_t kThreads>
 const void *norm_kernel(bool fp32) {
     if constexpr (kGrad)
-        return fp32 ? reinterpret_cast<const void *>(&afx_norm_grad_kernel<kTeam, kVec, I, float>)
-                    : reinterpret_cast<const void *>(&afx_norm_grad_kernel<kTeam, kVec, I, uint16_t>);
+        return fp32 ? reinterpret_cast<const void *>(&afx_norm_grad_kernel<kTeam, kVec, I, float, kThreads>)
+                    : reinterpret_cast<const void *>(&afx_norm_grad_kernel<kTeam, kVec, I, uint16_t, kThreads>);
     else
         return fp32 ? reinterpret_cast<const void *>(&afx_norm_kernel<kTeam, kVec, I, float>)
                     : reinterpret_cast<const void *>(&afx_norm_kernel<kTeam, kVec, I, uint16_t>);
 }
 template <bool kGrad, bool kVec>
 const void *norm_kernel(const NormShape &s, bool fp32) {
-    if (s.team == 16) return norm_kernel<kGrad, 16, kVec, 1>(fp32);
-    if (s.team == 64) return norm_kernel<kGrad, 64, kVec, 1>(fp32);
-    return s.iters == 1 ? norm_kernel<kGrad, 0, kVec, 1>(fp32) : norm_kernel<kGrad, 0, kVec, 4>(fp32);
+    if (s.team == 16) return norm_kernel<kGrad, 16, kVec, 1, kTeamThreads>(fp32);
+    if (s.team == 64) return norm_kernel<kGrad, 64, kVec, 1, kTeamThreads>(fp32);
+    if (s.iters == 4) return norm_kernel<kGrad, 0, kVec, 4, 1024>(fp32);
+    // (a workgroup of at most 12 waves has 168 registers a lane, one of 16 has 128)
+    return s.threads <= 768 ? norm_kernel<kGrad, 0, kVec, 1, 768>(fp32) : norm_kernel<kGrad, 0, kVec, 1, 1024>(fp32);
 }
 template <bool kGrad>
 int launch_norm(NormArgs &a, const NormShape &s, uint32_t blocks, bool vec, bool fp32, hipStream_t stream) {
@@ -414,7 +485,7 @@ int check_rows(const Rows *r, size_t n, uint32_t m, uint64_t d, size_t in0, size
 
 // Workgroups of the gradients' launch, and their partial sums.
 uint64_t norm_space(const afx_block_norm *p, uint32_t m) {
-    return (uint64_t)norm_blocks(norm_shape(p->d), m, kGradBlocks) * 3 * p->d * 4;
+    return (uint64_t)grad_blocks(norm_shape(p->d), m) * 3 * p->d * 4;
 }
 
 }  // namespace
@@ -550,7 +621,7 @@ int afx_block_norm_backward_async(const afx_block_norm *p, uint32_t m, const flo
     a.scale = p->scale;
     a.inv_d = 1.f / (float)p->d;
     const NormShape shape = norm_shape(p->d);
-    uint32_t blocks = norm_blocks(shape, m, kGradBlocks);
+    uint32_t blocks = grad_blocks(shape, m);
     if (m) {
         rc = launch_norm<true>(a, shape, blocks, vec, rb == 4, s);
         if (rc != AFX_OK) return rc;
