@@ -304,9 +304,14 @@ __global__ __launch_bounds__(kUnits *kWave) void afx_gemm_t_join_kernel(const TA
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = __builtin_bit_cast(uint16_t, (__bf16)v[e]);
     } else {
-        float *y = p.y32 + t * p.ldy + col;  // 4-byte aligned
+        float *y = p.y32 + t * p.ldy + col;
+        if (((p.ldy & 3) | (reinterpret_cast<uintptr_t>(p.y32) & 15)) == 0) {
+            f32x4 *y4 = reinterpret_cast<f32x4 *>(y);
+            *y4 = p.add ? *y4 + v : v;
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = p.add ? y[e] + v[e] : v[e];
+            for (int e = 0; e < 4; ++e) y[e] = p.add ? y[e] + v[e] : v[e];
+        }
     }
 }
 

@@ -107,47 +107,48 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t end) {
 
 // The outputs of one 32-token fragment: accumulator v of acc[i] of lane l is
 // weight row 32 i + 8 (v / 4) + 4 (l / 32) + v mod 4 of the wave's 64, and
-// token t (l mod 32 of the fragment).
+// token t (l mod 32 of the fragment). Here accumulators 4 q .. 4 q + 3 of both.
 template <int kEpi, uint32_t kAct>
-__device__ inline void write_outputs(const MmArgs &p, uint32_t n0, uint32_t wn, uint32_t half, uint32_t t,
-                                     const f32x16 (&acc)[2]) {
+__device__ inline void write_outputs(const MmArgs &p, uint32_t n0, uint32_t wn, uint32_t half, uint32_t t, uint32_t q,
+                                     const f32x4 (&acc)[2]) {
     if (t >= p.m) return;
     if constexpr (kEpi == kEpiGated) {
         const bool vec = ((p.ldh | p.ldgu) & 3) == 0 &&
                          ((reinterpret_cast<uintptr_t>(p.h) | reinterpret_cast<uintptr_t>(p.g) |
                            reinterpret_cast<uintptr_t>(p.u)) & 7) == 0;
+        const uint32_t f = n0 + 32 * wn + 8 * q + 4 * half;
+        if (f >= p.n) return;
+        const uint32_t n4 = p.n - f;
+        float g[4], u[4], h[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t f = n0 + 32 * wn + 8 * q + 4 * half;
-            if (f >= p.n) continue;
-            const uint32_t n4 = p.n - f;
-            float g[4], u[4], h[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                g[v] = acc[0][4 * q + v];
-                u[v] = acc[1][4 * q + v];
-                h[v] = act<kAct>(g[v]) * u[v];
-            }
-            store4(p.h + (uint64_t)t * p.ldh + f, h, n4, vec);
-            if (p.g) {
-                store4(p.g + (uint64_t)t * p.ldgu + f, g, n4, vec);
-                store4(p.u + (uint64_t)t * p.ldgu + f, u, n4, vec);
-            }
+        for (int v = 0; v < 4; ++v) {
+            g[v] = acc[0][v];
+            u[v] = acc[1][v];
+            h[v] = act<kAct>(g[v]) * u[v];
+        }
+        store4(p.h + (uint64_t)t * p.ldh + f, h, n4, vec);
+        if (p.g) {
+            store4(p.g + (uint64_t)t * p.ldgu + f, g, n4, vec);
+            store4(p.u + (uint64_t)t * p.ldgu + f, u, n4, vec);
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint32_t c = n0 + 64 * wn + 8 * q + 4 * half;
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t c = n0 + 64 * wn + 32 * i + 8 * q + 4 * half;
             if (c >= p.n) continue;  // n is a multiple of 8
-            const float v[4] = {acc[q / 4][4 * (q % 4)], acc[q / 4][4 * (q % 4) + 1], acc[q / 4][4 * (q % 4) + 2],
-                                acc[q / 4][4 * (q % 4) + 3]};
             if constexpr (kEpi == kEpiBf16) {
+                const float v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
                 store4(p.h + (uint64_t)t * p.ldh + c, v, 4,
                        (p.ldh & 3) == 0 && (reinterpret_cast<uintptr_t>(p.h) & 7) == 0);
             } else {
-                float *y = p.y32 + (uint64_t)t * p.ldh + c;  // 4-byte aligned
+                float *y = p.y32 + (uint64_t)t * p.ldh + c;
+                if (((p.ldh & 3) | (reinterpret_cast<uintptr_t>(p.y32) & 15)) == 0) {
+                    f32x4 *y4 = reinterpret_cast<f32x4 *>(y);
+                    *y4 = p.add ? *y4 + acc[i] : acc[i];
+                } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = p.add ? y[e] + v[e] : v[e];
+                    for (int e = 0; e < 4; ++e) y[e] = p.add ? y[e] + acc[i][e] : acc[i][e];
+                }
             }
         }
     }
@@ -333,46 +334,46 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
     }
 
     // ---- outputs, or a range's sums as they lie in the lanes ------------------
-    if (splits == 1) {
+    f32x4 *out = reinterpret_cast<f32x4 *>(p.partial) + ((uint64_t)r * p.plan.m_tiles + mt) * (8 * kMT * kMmThreads);
 #pragma unroll
-        for (int j = 0; j < kMT; ++j) {
-            const f32x16 v[2] = {acc[0][j], acc[1][j]};
-            write_outputs<kEpi, kAct>(p, n0, wn, half, m0 + (BM / 2) * wm + 32 * j + fr, v);
-        }
-    } else {
-        f32x4 *out = reinterpret_cast<f32x4 *>(p.partial) + ((uint64_t)r * p.plan.m_tiles + mt) * (8 * kMT * kMmThreads);
+    for (int j = 0; j < kMT; ++j)
 #pragma unroll
-        for (int j = 0; j < kMT; ++j)
+        for (int q = 0; q < 4; ++q) {
+            f32x4 v[2];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const f32x16 &v = acc[q / 4][j];
-                out[(8 * j + q) * kMmThreads + threadIdx.x] =
-                    f32x4{v[4 * (q % 4)], v[4 * (q % 4) + 1], v[4 * (q % 4) + 2], v[4 * (q % 4) + 3]};
+            for (int i = 0; i < 2; ++i)
+                v[i] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            if (splits == 1) {
+                write_outputs<kEpi, kAct>(p, n0, wn, half, m0 + (BM / 2) * wm + 32 * j + fr, q, v);
+            } else {
+                out[(8 * j + 2 * q) * kMmThreads + threadIdx.x] = v[0];
+                out[(8 * j + 2 * q + 1) * kMmThreads + threadIdx.x] = v[1];
             }
-    }
+        }
 }
 
-// One 32-token fragment of every wave of one of the rest's tiles: the ranges'
-// sums added in their order (the same bits on every run), then the outputs.
-template <int BM, int kEpi, uint32_t kAct>
+// One 32-token fragment of every wave of one of the rest's tiles, or a quarter
+// of it (kQ 4 or 1): the ranges' sums added in their order (the same bits on
+// every run), then the outputs.
+template <int BM, int kEpi, uint32_t kAct, int kQ>
 __global__ __launch_bounds__(kMmThreads) void afx_mm_join_kernel(const MmArgs p) {
-    constexpr int kMT = BM / 64;
-    const uint32_t j = blockIdx.x % kMT, mt = blockIdx.x / kMT % p.plan.m_tiles, nr = blockIdx.x / kMT / p.plan.m_tiles;
+    constexpr uint32_t kMT = BM / 64, kParts = 4 / kQ;
+    const uint32_t q0 = blockIdx.x % kParts * kQ, j = blockIdx.x / kParts % kMT;
+    const uint32_t mt = blockIdx.x / (kParts * kMT) % p.plan.m_tiles, nr = blockIdx.x / (kParts * kMT) / p.plan.m_tiles;
     const uint32_t lane = threadIdx.x & (kMmWave - 1), wave = threadIdx.x / kMmWave;
-    f32x16 acc[2] = {f32x16{}, f32x16{}};
-    for (uint32_t s = 0; s < p.plan.splits; ++s) {
-        const f32x4 *in = reinterpret_cast<const f32x4 *>(p.partial) +
-                          ((uint64_t)(nr * p.plan.splits + s) * p.plan.m_tiles + mt) * (8 * kMT * kMmThreads);
+    f32x4 acc[kQ][2] = {};
+    const uint64_t range = (uint64_t)p.plan.m_tiles * (8 * kMT * kMmThreads);  // from one to the next
+    const f32x4 *in = reinterpret_cast<const f32x4 *>(p.partial) + nr * p.plan.splits * range +
+                      (uint64_t)mt * (8 * kMT * kMmThreads) + (8 * j + 2 * q0) * kMmThreads + threadIdx.x;
+#pragma unroll(4 / kQ)
+    for (uint32_t s = 0; s < p.plan.splits; ++s)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const f32x4 v = in[(8 * j + q) * kMmThreads + threadIdx.x];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[q / 4][4 * (q % 4) + e] += v[e];
-        }
-    }
+        for (int k = 0; k < 2 * kQ; ++k) acc[k / 2][k % 2] += in[s * range + k * kMmThreads];
     constexpr uint32_t kOutN = kEpi == kEpiGated ? kBN / 2 : kBN;
-    write_outputs<kEpi, kAct>(p, (p.plan.n_full + nr) * kOutN, wave & 3, lane >> 5,
-                              mt * BM + (BM / 2) * (wave >> 2) + 32 * j + (lane & 31), acc);
+#pragma unroll
+    for (int k = 0; k < kQ; ++k)
+        write_outputs<kEpi, kAct>(p, (p.plan.n_full + nr) * kOutN, wave & 3, lane >> 5,
+                                  mt * BM + (BM / 2) * (wave >> 2) + 32 * j + (lane & 31), q0 + k, acc[k]);
 }
 
 // A CU runs one workgroup of these tiles, 32 CUs share an XCD. (On another
@@ -414,8 +415,14 @@ int launch(MmArgs &p, hipStream_t stream) {
                         dim3(kMmThreads), args, 0, stream) != hipSuccess)
         return AFX_E_HIP;
     if (q.splits == 1) return AFX_OK;
-    return hipLaunchKernel(reinterpret_cast<const void *>(&afx_mm_join_kernel<BM, kEpi, kAct>),
-                           dim3(q.n_rest * q.m_tiles * (BM / 64)), dim3(kMmThreads), args, 0, stream) == hipSuccess
+    // Whole fragments write whole lines (64 tiles of 256 tokens, gated: 16 us,
+    // 23 in quarters); few of them leave CUs idle and are quartered (6 tiles
+    // of 64 tokens: 13.8 us, 4.3 in quarters).
+    const uint32_t frags = q.n_rest * q.m_tiles * (BM / 64);
+    const bool whole = frags >= 256;
+    const void *join = whole ? reinterpret_cast<const void *>(&afx_mm_join_kernel<BM, kEpi, kAct, 4>)
+                             : reinterpret_cast<const void *>(&afx_mm_join_kernel<BM, kEpi, kAct, 1>);
+    return hipLaunchKernel(join, dim3(whole ? frags : 4 * frags), dim3(kMmThreads), args, 0, stream) == hipSuccess
                ? AFX_OK
                : AFX_E_HIP;
 }

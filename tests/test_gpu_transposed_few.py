@@ -49,6 +49,26 @@ def test_integers_exact(rows, cols, m):
     assert torch.equal(product(mat, d, m, True), want + 5)
 
 
+@pytest.mark.parametrize("m", [20, 70, 300])
+@pytest.mark.parametrize("cols", [136, 160])
+def test_outputs_aligned_to_their_elements_only(cols, m):
+    """y 4 bytes past a 16-byte boundary: the same bits as an aligned one."""
+    rng = rng_of(64, cols, m)
+    mat = Coded(normal(rng, (200, cols)))
+    d = torch.from_numpy(normal(rng, (m, 200))).to(torch.bfloat16).cuda()
+    n = afx.afx_restore_gemm_t_workspace(200, cols, m)
+    ws, got = workspace(n), []
+    for shift in (0, 1):
+        for add in (False, True):
+            y = torch.full((m * cols + 2,), 3.0, device="cuda")
+            afx.afx_restore_gemm_t_async(mat.info, mat.dev.data_ptr(), 200, cols, d.data_ptr(), m,
+                                         y.data_ptr() + 4 * shift, add, ws.data_ptr(), n, stream())
+            torch.cuda.synchronize()
+            assert bool((y[m * cols + shift:] == 3.0).all() and (y[:shift] == 3.0).all())
+            got.append(y[shift:m * cols + shift].clone())
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+
+
 @pytest.mark.parametrize("m", [3, 40])
 @pytest.mark.parametrize("rows,cols", [(40, 96), (200, 320)])
 def test_infinities_and_nan_stay_in_their_columns(rows, cols, m):
