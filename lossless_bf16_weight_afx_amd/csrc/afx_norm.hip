@@ -17,7 +17,9 @@
 // Memory bounds both: every value is read once and held in registers (FP32)
 // between the sums and the outputs. A team of 16 lanes (d <= 128), a wave
 // (d <= 512) or a workgroup of up to 16 waves takes a row; each lane holds 8
-// values (32 for d > 8192).
+// values, 16 for d > 8192, 32 for d > 16384. (The gradients keep nine values
+// for each; 32 of them do not fit the registers: 1024 x 16384, BF16, 342 us
+// with 32, 128 with 16.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -401,7 +403,7 @@ struct NormShape {
 NormShape norm_shape(uint64_t d) {
     if (d <= 128) return {16, kTeamThreads, kTeamThreads / 16, 1};
     if (d <= 512) return {64, kTeamThreads, kTeamThreads / 64, 1};
-    const uint32_t iters = d <= 8192 ? 1 : 4;
+    const uint32_t iters = d <= 8192 ? 1 : d <= 16384 ? 2 : 4;
     const uint32_t threads = (uint32_t)((d + 8 * iters * 64 - 1) / (8 * iters * 64) * 64);
     return {0, threads, 1, iters};
 }
@@ -426,6 +428,7 @@ template <bool kGrad, bool kVec>
 const void *norm_kernel(const NormShape &s, bool fp32) {
     if (s.team == 16) return norm_kernel<kGrad, 16, kVec, 1, kTeamThreads>(fp32);
     if (s.team == 64) return norm_kernel<kGrad, 64, kVec, 1, kTeamThreads>(fp32);
+    if (s.iters == 2) return norm_kernel<kGrad, 0, kVec, 2, 1024>(fp32);
     if (s.iters == 4) return norm_kernel<kGrad, 0, kVec, 4, 1024>(fp32);
     // (a workgroup of at most 12 waves has 168 registers a lane, one of 16 has 128)
     return s.threads <= 768 ? norm_kernel<kGrad, 0, kVec, 1, 768>(fp32) : norm_kernel<kGrad, 0, kVec, 1, 1024>(fp32);
