@@ -59,7 +59,7 @@ constexpr int kBufferFlags = 0x00020000;  // raw buffer, 32-bit data format
 // A unit is a weight tile, or one range of one of the rest; its token tiles
 // follow each other on one XCD, whose L2 then fetches the weights once.
 struct MmPlan {
-    uint32_t m_tiles, n_full, n_rest, splits;
+    uint32_t bm, m_tiles, n_full, n_rest, splits;  // bm: tokens of a tile
 };
 
 struct MmArgs {
@@ -380,13 +380,11 @@ __global__ __launch_bounds__(kMmThreads) void afx_mm_join_kernel(const MmArgs p)
 // device the launches do the same work in another number of rounds: the plan,
 // and so the workspace and the order of the sums, do not depend on it.)
 constexpr uint32_t kXcds = 8, kXcdCus = 32;
-constexpr uint32_t kLeastRange = 8;  // k-tiles: a range's start and join take about as long as 4
+constexpr uint32_t kLeastRange = 4;  // k-tiles: a range's start and join take about as long
 
-uint32_t tokens_per_tile(uint32_t m) { return m <= 64 ? 64 : m <= 128 ? 128 : 256; }
-
-MmPlan mm_plan(uint32_t m, uint64_t n, uint32_t out_n, uint64_t k_tiles) {
-    const uint32_t bm = tokens_per_tile(m);
+MmPlan plan_for(uint32_t bm, uint32_t m, uint64_t n, uint32_t out_n, uint64_t k_tiles) {
     MmPlan p{};
+    p.bm = bm;
     p.m_tiles = (m + bm - 1) / bm;
     const uint32_t n_tiles = (uint32_t)((n + out_n - 1) / out_n);
     // weight tiles of a round: what every XCD's CUs take at once
@@ -400,8 +398,35 @@ MmPlan mm_plan(uint32_t m, uint64_t n, uint32_t out_n, uint64_t k_tiles) {
     return p;
 }
 
-uint64_t partial_bytes(const MmPlan &p, uint32_t m) {
-    return p.splits > 1 ? (uint64_t)p.n_rest * p.splits * p.m_tiles * tokens_per_tile(m) * kBN * 4 : 0;
+// Tokens of a tile: 64, 128 or 256, whichever is estimated to take least. A
+// k-tile takes about 1.2, 1.4 and 1.75 us of them (17408 x 5112 weights, as
+// many tokens: 97, 110 and 138 us), so that large tiles win where they fill
+// the CUs, small ones where large ones would not. The sums of ranges cost
+// about 4 us and their bytes' way to memory and back. (Gated, with join:
+// 1000 x 600 weights, 200 tokens 11.7 us, 16.9 with the largest tile; 3000 x
+// 1000, 600 tokens: 21 and 32; 17408 x 5120, 256 tokens, where the two are
+// estimated alike: 141 and 136.)
+MmPlan mm_plan(uint32_t m, uint64_t n, uint32_t out_n, uint64_t k_tiles) {
+    MmPlan best{};
+    double least = 0;
+    for (uint32_t bm = 64; bm <= 256; bm *= 2) {
+        const MmPlan p = plan_for(bm, m, n, out_n, k_tiles);
+        const auto rounds = [&](uint64_t units) { return (double)((units * p.m_tiles + 255) / 256); };
+        double tiles = rounds(p.n_full) * (double)k_tiles, us = 0;
+        if (p.n_rest) tiles += rounds((uint64_t)p.n_rest * p.splits) * (double)((k_tiles + p.splits - 1) / p.splits);
+        if (p.splits > 1) us += 4 + (double)p.n_rest * p.splits * p.m_tiles * bm * kBN * 8 / 4.9e6;
+        us += tiles * (bm == 64 ? 1.2 : bm == 128 ? 1.4 : 1.75);
+        if (bm == 64 || us < least) {
+            best = p;
+            least = us;
+        }
+        if (m <= bm) break;  // a larger tile would be part empty
+    }
+    return best;
+}
+
+uint64_t partial_bytes(const MmPlan &p) {
+    return p.splits > 1 ? (uint64_t)p.n_rest * p.splits * p.m_tiles * p.bm * kBN * 4 : 0;
 }
 
 template <int BM, bool kNN, int kEpi, uint32_t kAct>
@@ -429,7 +454,7 @@ int launch(MmArgs &p, hipStream_t stream) {
 
 template <bool kNN, int kEpi, uint32_t kAct = 0>
 int launch_for_tokens(MmArgs &p, hipStream_t stream) {
-    switch (tokens_per_tile(p.m)) {
+    switch (p.plan.bm) {
         case 64: return launch<64, kNN, kEpi, kAct>(p, stream);
         case 128: return launch<128, kNN, kEpi, kAct>(p, stream);
         default: return launch<256, kNN, kEpi, kAct>(p, stream);
@@ -444,10 +469,10 @@ MmPlan transposed_plan(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m
 }  // namespace
 
 uint64_t mm_gated_partial(uint64_t rows, uint64_t cols, uint32_t m) {
-    return partial_bytes(gated_plan(rows, cols, m), m);
+    return partial_bytes(gated_plan(rows, cols, m));
 }
 uint64_t mm_transposed_partial(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
-    return partial_bytes(transposed_plan(rows, cols, n_mats, m), m);
+    return partial_bytes(transposed_plan(rows, cols, n_mats, m));
 }
 
 int launch_mm_gated(const MmGated &q, hipStream_t stream) {

@@ -33,6 +33,16 @@ class FeedForward:
                  act: int = afx.ACT_SILU, eps: float = 1e-6, scale: float = 1.0, max_tokens: int, training=False):
         import torch
 
+        if d % 64 or ff % 256 or d < 64 or ff < 256:
+            raise ValueError(f"d {d} and ff {ff}: the down product takes multiples of 64 and 256")
+        if any(int(info.n_elems) != d * ff for info, _ in (gate, up, down)):
+            raise ValueError(f"a matrix does not have {d} x {ff} values")
+        if max_tokens < 1:
+            raise ValueError("max_tokens must be at least 1")
+        for t in (w_pre, w_post, block_gate, w_next):
+            if t is not None and (t.dtype != torch.bfloat16 or t.shape != (d,) or not t.is_contiguous()
+                                  or t.device != w_pre.device):
+                raise ValueError(f"norm weights and the gate are contiguous BF16 [{d}] tensors on one device")
         self.gate, self.up, self.down, self.d, self.ff = gate, up, down, d, ff
         self.vectors = (w_pre, w_post, block_gate, w_next)  # (kept: the structs below hold addresses)
         addr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
@@ -43,7 +53,8 @@ class FeedForward:
         new = lambda n, t=torch.bfloat16: torch.empty((max_tokens, n), dtype=t, device=dev)  # noqa: E731
         self.xn, self.h, self.b, self.r_out = new(d), new(ff), new(d, torch.float32), new(d)
         self.xn_next = new(d) if w_next is not None else None
-        # a workspace's size need not grow with the tokens: the largest of those up to max_tokens
+        # A workspace's size need not grow with the tokens (other kernels, other divisions of the work), but it does
+        # within a tile of tokens: the largest is at one of these.
         sizes = [afx.afx_restore_gated_workspace(ff, d, m) for m in self._sizes()]
         self.training = training
         if training:
@@ -58,7 +69,8 @@ class FeedForward:
         self.ws = torch.empty(max(max(sizes), 16), dtype=torch.uint8, device=dev)
 
     def _sizes(self):
-        return range(1, self.max_tokens + 1)
+        n = self.max_tokens
+        return sorted({*range(1, min(n, 256) + 1), *range(256, n + 1, 256), n})
 
     def _stream(self, m: int) -> int:
         import torch

@@ -204,6 +204,22 @@ def test_refusals():
             t.ffn.backward(r, *grads)
     with pytest.raises(afx.AfxError):
         t.ffn.forward(r[:1].expand(8, D))  # rows that share memory
+    mats, w = [c.pair for c in t.mats], t.vectors[0]
+    for bad in (dict(d=D + 8), dict(ff=FF - 256), dict(max_tokens=0), dict(w_pre=w.float()), dict(w_pre=w[:-1]),
+                dict(w_next=w.cpu()), dict(block_gate=torch.ones(2 * D, dtype=torch.bfloat16, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            ffn.FeedForward(*mats, **{**dict(d=D, ff=FF, w_pre=w, max_tokens=8), **bad})
+
+
+def test_workspace_is_the_largest_of_all_token_counts():
+    """A size between the ones the constructor looks at never needs more."""
+    t = Block(10, 700)
+    need = 0
+    for m in range(1, 701):
+        need = max(need, afx.afx_restore_gated_workspace(FF, D, m), afx.afx_restore_gated_workspace(FF, D, m, True),
+                   afx.afx_restore_gemm_t_workspace(D, FF, m), afx.afx_block_norm_workspace(t.ffn.norm_in, m),
+                   afx.afx_block_norm_workspace(t.ffn.norm_out, m))
+    assert t.ffn.ws.numel() == need
 
 
 @pytest.mark.parametrize("m", [1, 4, 16, 64, 100, 150])
