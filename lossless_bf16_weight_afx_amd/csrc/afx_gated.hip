@@ -244,9 +244,7 @@ int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_de
     if (path == kPathGemm) return launch_gated_gemm(*w, {x_dev, x_stride, m, h_dev, g_dev, u_dev, h_stride, gus}, ws, s);
     const PanelJob jobs[2] = {{w->gate_info, w->gate_blob_dev, w->rows, w->cols, u16_at(ws, sp.wg)},
                               {w->up_info, w->up_blob_dev, w->rows, w->cols, u16_at(ws, sp.wu)}};
-    rc = launch_restore_panels(jobs, 2, s);
-    if (rc != AFX_OK) return rc;
-    rc = launch_pack_panels(x_dev, x_stride, m, w->cols, u16_at(ws, sp.a0), s);
+    rc = launch_panels(jobs, x_dev, x_stride, m, u16_at(ws, sp.a0), s);
     if (rc != AFX_OK) return rc;
     MmGated p{};
     p.x = u16_at(ws, sp.a0);

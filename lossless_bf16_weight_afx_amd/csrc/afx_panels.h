@@ -25,10 +25,10 @@ struct PanelJob {
     uint64_t rows, cols;
     uint16_t *out;  // panel_bytes(rows, cols)
 };
-int launch_restore_panels(const PanelJob *jobs, uint32_t n, hipStream_t stream);  // n <= 2
 
-// Rows of a [m, cols] (BF16, row stride ld, a multiple of 8; 16-byte aligned;
-// cols a multiple of 8) as panels.
-int launch_pack_panels(const uint16_t *a, uint64_t ld, uint32_t m, uint64_t cols, uint16_t *out, hipStream_t stream);
+// Restores both matrices (of the same size) and copies the rows of a [m,
+// cols] (BF16, row stride ld, a multiple of 8; 16-byte aligned) to panels.
+int launch_panels(const PanelJob (&jobs)[2], const uint16_t *a, uint64_t ld, uint32_t m, uint16_t *out,
+                  hipStream_t stream);
 
 }  // namespace afx

@@ -40,24 +40,32 @@ struct OutPlace {
 namespace afx {
 namespace {
 
-// Zeros in the last panel's columns past the matrix's.
-__global__ __launch_bounds__(256) void afx_panel_pad_kernel(uint16_t *panel, uint64_t rows, uint32_t used) {
-    const uint64_t r = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    if (r >= rows) return;
-    for (uint32_t c = used; c < kPanelCols; c += 8)
-        *reinterpret_cast<uint4 *>(panel + r * kPanelCols + c) = make_uint4(0, 0, 0, 0);
-}
+struct PackArgs {
+    const uint16_t *a;  // [m, cols], row stride ld
+    uint64_t ld, cols, padded;
+    uint16_t *out;
+    uint16_t *w[2];     // panels of two coded matrices [rows, cols]
+    uint64_t rows;
+    uint32_t m;
+};
 
-// 8 values per thread; a wave reads 1 KB of a row and writes 8 panels' 128
-// bytes of it.
-__global__ __launch_bounds__(256) void afx_pack_panels_kernel(const uint16_t *a, uint64_t ld, uint32_t m, uint64_t cols,
-                                                              uint64_t padded, uint16_t *out) {
+// Activations to panels, 8 values per thread: a wave reads 1 KB of a row and
+// writes 8 panels' 128 bytes of it. And zeros in the last panel's columns of
+// both matrices past theirs (the restore writes only theirs).
+__global__ __launch_bounds__(256) void afx_pack_panels_kernel(const PackArgs p) {
     const uint64_t c = 8 * ((uint64_t)blockIdx.x * 256 + threadIdx.x);
-    if (c >= padded) return;
-    for (uint64_t t = blockIdx.y; t < m; t += gridDim.y) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < cols) v = *reinterpret_cast<const uint4 *>(a + t * ld + c);
-        *reinterpret_cast<uint4 *>(out + ((c / kPanelCols) * m + t) * kPanelCols + c % kPanelCols) = v;
+    if (c < p.padded)
+        for (uint64_t t = blockIdx.y; t < p.m; t += gridDim.y) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (c < p.cols) v = *reinterpret_cast<const uint4 *>(p.a + t * p.ld + c);
+            *reinterpret_cast<uint4 *>(p.out + ((c / kPanelCols) * p.m + t) * kPanelCols + c % kPanelCols) = v;
+        }
+    if (p.cols == p.padded) return;
+    const uint64_t last = p.cols / kPanelCols * p.rows * kPanelCols, threads = (uint64_t)gridDim.x * gridDim.y * 256;
+    for (uint64_t r = ((uint64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x; r < 2 * p.rows; r += threads) {
+        uint16_t *row = (r < p.rows ? p.w[0] : p.w[1]) + last + (r < p.rows ? r : r - p.rows) * kPanelCols;
+        for (uint32_t k = p.cols % kPanelCols; k < kPanelCols; k += 8)
+            *reinterpret_cast<uint4 *>(row + k) = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -67,7 +75,9 @@ bool launch(const void *fn, dim3 grid, uint32_t threads, void **args, hipStream_
 
 }  // namespace
 
-int launch_restore_panels(const PanelJob *jobs, uint32_t n, hipStream_t stream) {
+int launch_panels(const PanelJob (&jobs)[2], const uint16_t *a, uint64_t ld, uint32_t m, uint16_t *out,
+                  hipStream_t stream) {
+    constexpr uint32_t n = 2;
     Batch batch;
     batch.n_tensors = n;
     uint64_t chunks[2];
@@ -87,24 +97,19 @@ int launch_restore_panels(const PanelJob *jobs, uint32_t n, hipStream_t stream) 
     }
     void *args[] = {&batch};
     if (!launch(reinterpret_cast<const void *>(&afx_decode_kernel), dim3(grid), kThreads, args, stream)) return AFX_E_HIP;
-    for (uint32_t t = 0; t < n; ++t) {
-        uint32_t used = (uint32_t)(jobs[t].cols % kPanelCols);
-        if (!used) continue;
-        uint64_t rows = jobs[t].rows;
-        uint16_t *panel = jobs[t].out + jobs[t].cols / kPanelCols * rows * kPanelCols;
-        void *pad_args[] = {&panel, &rows, &used};
-        if (!launch(reinterpret_cast<const void *>(&afx_panel_pad_kernel), dim3((unsigned)((rows + 255) / 256)), 256,
-                    pad_args, stream))
-            return AFX_E_HIP;
-    }
-    return AFX_OK;
-}
-
-int launch_pack_panels(const uint16_t *a, uint64_t ld, uint32_t m, uint64_t cols, uint16_t *out, hipStream_t stream) {
-    uint64_t padded = panel_count(cols) * kPanelCols;
-    void *args[] = {&a, &ld, &m, &cols, &padded, &out};
+    PackArgs p{};
+    p.a = a;
+    p.ld = ld;
+    p.cols = jobs[0].cols;
+    p.padded = panel_count(p.cols) * kPanelCols;
+    p.out = out;
+    p.w[0] = jobs[0].out;
+    p.w[1] = jobs[1].out;
+    p.rows = jobs[0].rows;
+    p.m = m;
+    void *pack_args[] = {&p};
     return launch(reinterpret_cast<const void *>(&afx_pack_panels_kernel),
-                  dim3((unsigned)((padded / 8 + 255) / 256), std::min(m, 32768u)), 256, args, stream)
+                  dim3((unsigned)((p.padded / 8 + 255) / 256), std::min(m, 32768u)), 256, pack_args, stream)
                ? AFX_OK
                : AFX_E_HIP;
 }
