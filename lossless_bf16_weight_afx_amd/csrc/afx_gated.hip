@@ -154,11 +154,15 @@ GatedPath gated_path(uint64_t cols, uint32_t m) {
 }
 
 // Whether a transposed product takes the coded matrices as they are, or has
-// them restored to the workspace first (the gradient of two 17408 x 5120
-// matrices, fused and restored: 16 tokens 107 and 211 us, 64 138 and 215;
-// 5120 x 17408, 64 tokens: 78 and 110. Above 64 the fused kernel's sums would
-// not fit its registers.)
-bool transposed_fused(uint64_t cols, uint32_t m) { return m <= kGemmTTokens && cols % kGroup == 0; }
+// them restored to the workspace first. Fused and restored, rows of whole
+// groups: the gradient of two 17408 x 5120 matrices, 16 tokens 107 and 211
+// us, 64 138 and 215; 5120 x 17408, 64 tokens: 78 and 110. (Above 64 the fused
+// kernel's sums would not fit its registers.) Other rows decode a third more:
+// 5120 x 17400, 16 tokens: 76 and 111; but 37 tokens and two 4100 x 1528
+// matrices 37 and 34, 64 and 17408 x 5112 202 and 206.
+bool transposed_fused(uint64_t cols, uint32_t m) {
+    return m <= (cols % kGroup == 0 ? kGemmTTokens : kGemmTTokensSplit);
+}
 
 // Where the pieces of a gated call's workspace lie, and its size.
 struct GatedSpace {

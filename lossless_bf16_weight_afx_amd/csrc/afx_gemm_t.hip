@@ -1,4 +1,4 @@
-// afx_gemm_t.hip -- y = d W for up to 64 tokens (gfx950), W restored and
+// afx_gemm_t.hip -- y = d W for few tokens (gfx950), W restored and
 // multiplied on the matrix cores without reaching memory: the transposed
 // product, whose reduction runs along W's rows, one below the other.
 //
@@ -31,9 +31,13 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-constexpr uint32_t kTRows = 32, kTCols = 128;  // a slab
+constexpr uint32_t kTRows = 32, kTCols = 128;  // a slab as it is decoded
 constexpr uint32_t kTok = 16;                  // tokens of an operand
-constexpr uint32_t kUnits = kTCols / 16;       // columns of a matrix instruction
+// Columns of a slab that are multiplied: all, or, where rows are not whole
+// groups and so start up to 24 values into one, 96, which 4 groups cover
+// wherever the row starts.
+constexpr uint32_t slab_cols(bool whole) { return whole ? kTCols : kTCols - kGroup; }
+constexpr uint32_t slab_units(bool whole) { return slab_cols(whole) / 16; }  // 16: columns of a matrix instruction
 // Column slabs that a workgroup's waves take side by side. The lines that
 // hold a row's code words and gaps are then read by waves of one CU at about
 // the same time; more of them leave fewer waves to add their sums in LDS,
@@ -53,7 +57,7 @@ static_assert(chain_word(32 * kRowRev + kLead - kRowMaxStart - 32 * kMaxLen) >= 
 constexpr uint32_t kSmRow = kTCols + 16;       // a row's sign/mantissa bytes in LDS
 constexpr uint32_t kStage = kTRows * (kSmRow + kTCols);  // bytes of LDS of a wave: the sign/mantissa bytes and half
                                                          // the restored slab
-static_assert(kTRows * kRowSlice * 4 <= kStage && kUnits * 64 * 16 <= kStage && kTRows * kSmRow % 256 == 0 &&
+static_assert(kTRows * kRowSlice * 4 <= kStage && slab_units(true) * 64 * 16 <= kStage && kTRows * kSmRow % 256 == 0 &&
               kSmRow >= kTCols, "so do the words, or 16 tokens' sums; rows stay aligned to the banks");
 
 struct TArgs {
@@ -79,9 +83,9 @@ __device__ inline uint32_t piece_at(uint32_t r, uint32_t piece) {
     return r * (kTCols * 2) + 32 * ((piece >> 1) ^ row_swizzle(r)) + 16 * ((piece & 1) ^ ((r >> 2) & 1));
 }
 
-template <int kTB, int kWavesWG>
+template <int kTB, int kWavesWG, bool kWhole>
 __global__ __launch_bounds__(kWavesWG *kWave, kWavesWG / 4) void afx_gemm_t_kernel(const TArgs p) {
-    constexpr uint32_t kRowWaves = kWavesWG / kColWaves;
+    constexpr uint32_t kRowWaves = kWavesWG / kColWaves, kCols = slab_cols(kWhole), kUnits = slab_units(kWhole);
     struct Lds {
         uint32_t plut[kLutEntries];  // 16 KB, at address 0 (afx_gemv_body.h)
         uint32_t stage[kWavesWG][kStage / 4];
@@ -123,24 +127,38 @@ __global__ __launch_bounds__(kWavesWG *kWave, kWavesWG / 4) void afx_gemm_t_kern
     auto put = [&](uint32_t i, uint4 v) {  // words i .. i + 3, reversed
         *reinterpret_cast<uint4 *>(seg_w + kRowRev - 3 - i) = make_uint4(v.w, v.z, v.y, v.x);
     };
-    auto col0_of = [&](At a) { return min(a.t * kColWaves + wc, p.col_slabs - 1) * kTCols; };
-    auto tile_of = [&](At a) { return tile_at(T, (uint64_t)a.b * kTRows * p.cols + col0_of(a)); };
-    auto len_of = [&](At a) { return umin32(kTCols, p.cols - col0_of(a)); };
+    auto col0_of = [&](At a) { return min(a.t * kColWaves + wc, p.col_slabs - 1) * kCols; };
+    auto e0_of = [&](At a) { return (uint64_t)a.b * kTRows * p.cols + col0_of(a); };
+    // (from the group that the slab's first value lies in)
+    auto tile_of = [&](At a) { return tile_at(T, e0_of(a) & ~(uint64_t)(kGroup - 1)); };
+    // Rows past the matrix repeat the last one.
     auto row_of = [&](At a, uint32_t r) { return umin32(r, p.rows - 1 - a.b * kTRows) * p.cols; };
+    auto shift_of = [&](At a, uint32_t r) {  // columns between the first group's start and the slab's first
+        return kWhole ? 0u : ((uint32_t)e0_of(a) + row_of(a, r)) & (kGroup - 1);
+    };
+    auto seg_of = [&](At a, uint32_t r) {
+        if constexpr (kWhole) return Seg{row_of(a, r), umin32(kTCols, p.cols - col0_of(a))};
+        const uint32_t start = (((uint32_t)e0_of(a) & (kGroup - 1)) + row_of(a, r)) & ~(kGroup - 1);
+        const uint32_t left = (tile_of(a).left + kGroup - 1) & ~(kGroup - 1);  // the last group may be part empty
+        return Seg{start, umin32(kTCols, left - start)};
+    };
 
     Words words;
     Bits bits;
     u32x4 w0, w1, sm[4];
-    auto load_bits = [&](At a) { bits = seg_bits(tile_of(a), Seg{row_of(a, lrow), len_of(a)}, c); };
+    auto load_bits = [&](At a) { bits = seg_bits(tile_of(a), seg_of(a, lrow), c); };
     auto load_words = [&] {
         w0 = __builtin_bit_cast(u32x4, load_words4(T, words.wa + 4 * c));
         w1 = __builtin_bit_cast(u32x4, load_words4(T, words.wa + 8 + 4 * c));
     };
     auto load_sm = [&](At a) {  // 8 lanes a row; read once: not kept in the caches
-        const uint8_t *at = tile_of(a).sm + umin32(16 * (lane & 7), len_of(a) - 16);
+        const uint8_t *at = tile_of(a).sm;
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i)
-            sm[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at + row_of(a, 8 * i + (lane >> 3))));
+        for (uint32_t i = 0; i < 4; ++i) {
+            const Seg g = seg_of(a, 8 * i + (lane >> 3));
+            sm[i] = __builtin_nontemporal_load(
+                reinterpret_cast<const u32x4 *>(at + g.start + umin32(16 * (lane & 7), g.len - 16)));
+        }
     };
     // Tokens past the last, and rows past d's, come as zeros.
     constexpr uint32_t kPastEnd = 0x80000000u;
@@ -238,9 +256,15 @@ __global__ __launch_bounds__(kWavesWG *kWave, kWavesWG / 4) void afx_gemm_t_kern
                     join4(b.w & in, ex[h][2 * j + 3] & in, wf[j + 1].z, wf[j + 1].w);
                 }
                 if (h == 1) wave_sync();  // the bytes have been read
+                uint8_t *half = stage + (h == 0 ? kTRows * kSmRow : 0);
+                const uint32_t first = 4 * (ln >> 4) - shift_of(cur, 16 * h + (ln & 15)) / 8;  // the lane's first piece
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4 *>(stage + (h == 0 ? kTRows * kSmRow : 0) + (put_at ^ (16 * j))) = wf[j];
+                for (uint32_t j = 0; j < 4; ++j) {
+                    if constexpr (kWhole)
+                        *reinterpret_cast<uint4 *>(half + (put_at ^ (16 * j))) = wf[j];
+                    else if (first + j < kCols / 8)  // (before the slab: a large number)
+                        *reinterpret_cast<uint4 *>(half + piece_at(ln & 15, first + j)) = wf[j];
+                }
             }
             wave_sync();
             // Columns 16 u .. of rows 8 q .. 8 q + 7, transposed: 16 lanes read
@@ -286,19 +310,24 @@ __global__ __launch_bounds__(kWavesWG *kWave, kWavesWG / 4) void afx_gemm_t_kern
     }
 }
 
-// 128 columns of 16 tokens: both matrices' ranges in order.
-__global__ __launch_bounds__(kUnits *kWave) void afx_gemm_t_join_kernel(const TArgs p, uint32_t blocks) {
+// A slab's columns of 16 tokens: both matrices' ranges in order.
+template <bool kWhole>
+__global__ __launch_bounds__(slab_units(kWhole) * kWave) void afx_gemm_t_join_kernel(const TArgs p, uint32_t blocks) {
+    constexpr uint32_t kCols = slab_cols(kWhole), kUnits = slab_units(kWhole);
     const uint32_t tile = blockIdx.x / kColWaves, cw = blockIdx.x % kColWaves, tb = blockIdx.y;
     const uint32_t lane = threadIdx.x % kWave, t = tb * kTok + (lane & 15);
-    const uint32_t col = blockIdx.x * kTCols + 16 * (threadIdx.x / kWave) + 4 * (lane >> 4);
+    const uint32_t col = blockIdx.x * kCols + 16 * (threadIdx.x / kWave) + 4 * (lane >> 4);
     if (t >= p.m || col >= p.cols) return;
     const uint32_t first = range_of(p.split, tile * p.split.tile_slabs);
     const uint32_t n = range_of(p.split, (tile + 1) * p.split.tile_slabs - 1) - first + 1;
     f32x4 v = f32x4{};
-    for (uint32_t mat = 0; mat < p.n_mats; ++mat)
-        for (uint32_t o = 0; o < n; ++o)
-            v += reinterpret_cast<const f32x4 *>(p.part + mat * p.part_mat)
-                [((part_place(p.split, tile, o, 0) * blocks + tb) * kColWaves + cw) * (kUnits * kWave) + threadIdx.x];
+    for (uint32_t mat = 0; mat < p.n_mats; ++mat) {
+        const f32x4 *in = reinterpret_cast<const f32x4 *>(p.part + mat * p.part_mat) +
+                          ((part_place(p.split, tile, 0, 0) * blocks + tb) * kColWaves + cw) * (kUnits * kWave) +
+                          threadIdx.x;
+#pragma unroll 8
+        for (uint32_t o = 0; o < n; ++o) v += in[(uint64_t)o * blocks * kColWaves * (kUnits * kWave)];
+    }
     if (p.y16) {
         uint16_t *y = p.y16 + t * p.ldy + col;
 #pragma unroll
@@ -317,23 +346,52 @@ __global__ __launch_bounds__(kUnits *kWave) void afx_gemm_t_join_kernel(const TA
 
 uint32_t token_blocks(uint32_t m) { return (m + kTok - 1) / kTok; }
 
-// One workgroup per CU of 256, divided between the matrices. (On a device with
-// fewer the rest follow: the split does not depend on the device.)
-GatedSplit t_split(uint64_t rows, uint64_t cols, uint32_t n_mats) {
+// Waves of a workgroup: 128 registers a lane hold 16 tokens' sums, 256 more.
+uint32_t workgroup_waves(uint32_t m) { return m <= kTok ? 16 : 8; }
+
+// One workgroup per CU of 256, divided between the matrices, and no more than
+// have a slab for each of their waves down a tile (1000 x 1000, 20 tokens: 24
+// us with one slab a workgroup, 17 so). On a device with fewer CUs the rest
+// follow: the split does not depend on the device.
+bool whole_groups(uint64_t cols) { return cols % kGroup == 0; }
+uint32_t col_slabs(uint64_t cols) {
+    const uint32_t each = slab_cols(whole_groups(cols));
+    return (uint32_t)((cols + each - 1) / each);
+}
+GatedSplit t_split(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
     GatedSplit s{};
     s.waves = 1;
     s.tile_slabs = (uint32_t)((rows + kTRows - 1) / kTRows);
-    s.tiles = s.row_tiles = (uint32_t)((cols + kTCols * kColWaves - 1) / (kTCols * kColWaves));
-    return with_ranges(s, 256 / n_mats);
+    s.tiles = s.row_tiles = (col_slabs(cols) + kColWaves - 1) / kColWaves;
+    const uint64_t each = (uint64_t)s.tiles * s.tile_slabs / (workgroup_waves(m) / kColWaves);
+    return with_ranges(s, (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(each, 256 / n_mats)));
 }
-uint64_t part_floats(const GatedSplit &s, uint32_t m) {
-    return part_places(s) * token_blocks(m) * kColWaves * kTCols * kTok;
+uint64_t part_floats(const GatedSplit &s, uint64_t cols, uint32_t m) {
+    return part_places(s) * token_blocks(m) * kColWaves * slab_cols(whole_groups(cols)) * kTok;
+}
+
+template <bool kWhole>
+int launch(TArgs &p, uint32_t blocks, hipStream_t stream) {
+    const void *fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<1, 16, kWhole>);
+    if constexpr (kWhole) {
+        if (blocks == 2) fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<2, 8, true>);
+        if (blocks == 3) fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<3, 8, true>);
+        if (blocks == 4) fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<4, 8, true>);
+    }
+    const uint32_t grid = p.n_mats * (p.n_mats == 2 ? (p.split.ranges + 7) / 8 * 8 : p.split.ranges);
+    void *args[] = {&p};  // hipLaunchKernel reports this launch's own status
+    if (hipLaunchKernel(fn, dim3(grid), dim3(workgroup_waves(p.m) * kWave), args, 0, stream) != hipSuccess) return AFX_E_HIP;
+    void *join_args[] = {&p, &blocks};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&afx_gemm_t_join_kernel<kWhole>), dim3(p.col_slabs, blocks),
+                           dim3(slab_units(kWhole) * kWave), join_args, 0, stream) == hipSuccess
+               ? AFX_OK
+               : AFX_E_HIP;
 }
 
 }  // namespace
 
 uint64_t gemm_t_space(uint64_t rows, uint64_t cols, uint32_t n_mats, uint32_t m) {
-    return n_mats * part_floats(t_split(rows, cols, n_mats), m) * 4;
+    return n_mats * part_floats(t_split(rows, cols, n_mats, m), cols, m) * 4;
 }
 
 int launch_gemm_t(const GemmT &q, uint8_t *ws, hipStream_t stream) {
@@ -343,35 +401,21 @@ int launch_gemm_t(const GemmT &q, uint8_t *ws, hipStream_t stream) {
         p.d[i] = q.d[i];
     }
     p.lda = q.lda;
-    p.split = t_split(q.rows, q.cols, q.n_mats);
+    p.split = t_split(q.rows, q.cols, q.n_mats, q.m);
     p.part = reinterpret_cast<float *>(ws);
-    p.part_mat = part_floats(p.split, q.m);
+    p.part_mat = part_floats(p.split, q.cols, q.m);
     p.n_mats = q.n_mats;
     p.m = q.m;
     p.rows = (uint32_t)q.rows;
     p.cols = (uint32_t)q.cols;
     p.ak = (uint32_t)((q.rows + 7) / 8 * 8);
-    p.col_slabs = (uint32_t)((q.cols + kTCols - 1) / kTCols);
+    p.col_slabs = col_slabs(q.cols);
     p.y32 = q.y32;
     p.y16 = q.y16;
     p.ldy = q.ldy;
     p.add = q.add;
-    uint32_t blocks = token_blocks(q.m);
-    const void *fn;
-    switch (blocks) {
-        case 1: fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<1, 16>); break;
-        case 2: fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<2, 8>); break;
-        case 3: fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<3, 8>); break;
-        default: fn = reinterpret_cast<const void *>(&afx_gemm_t_kernel<4, 8>); break;
-    }
-    const uint32_t grid = q.n_mats * (q.n_mats == 2 ? (p.split.ranges + 7) / 8 * 8 : p.split.ranges);
-    void *args[] = {&p};  // hipLaunchKernel reports this launch's own status
-    if (hipLaunchKernel(fn, dim3(grid), dim3(blocks == 1 ? 1024 : 512), args, 0, stream) != hipSuccess) return AFX_E_HIP;
-    void *join_args[] = {&p, &blocks};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&afx_gemm_t_join_kernel), dim3(p.col_slabs, blocks),
-                           dim3(kUnits * kWave), join_args, 0, stream) == hipSuccess
-               ? AFX_OK
-               : AFX_E_HIP;
+    const uint32_t blocks = token_blocks(q.m);
+    return whole_groups(q.cols) ? launch<true>(p, blocks, stream) : launch<false>(p, blocks, stream);
 }
 
 }  // namespace afx

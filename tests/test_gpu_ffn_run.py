@@ -222,14 +222,15 @@ def test_workspace_is_the_largest_of_all_token_counts():
     assert t.ffn.ws.numel() == need
 
 
+@pytest.mark.parametrize("cols", [1312, 1320])
 @pytest.mark.parametrize("m", [1, 4, 16, 64, 100, 150])
 @pytest.mark.parametrize("what", KINDS)
-def test_damaged_device_blobs_stay_in_bounds(what, m):
+def test_damaged_device_blobs_stay_in_bounds(what, m, cols):
     """Device copies that differ from the validated host blobs give wrong
     results, never an access out of bounds: guards around every output stay."""
     say(f"[gpu] case damaged blob: {what}, m={m}")
     rng = np.random.default_rng([KINDS.index(what), m, 11])
-    rows, cols = 144, 1312  # ends inside a tile of rows and a slab of columns; whole groups
+    rows = 144  # ends inside a tile of rows, as the columns do inside a slab
     mats = [Coded(rng, rows, cols, 0.05) for _ in range(2)]
     (gi, _), (ui, _) = (c.pair for c in mats)
     bad = [afx.to_device(damage(c.blob, what, rng)) for c in mats]

@@ -1,5 +1,4 @@
-"""GPU parity of the transposed products for few tokens (up to 64, rows of
-whole groups), where the coded matrix is multiplied as it is: small integers,
+"""GPU parity of the transposed products for few tokens (up to 64), where the coded matrix is multiplied as it is: small integers,
 so that every FP32 sum is exact and the 64-bit result is the answer; and
 infinities and NaN at the matrix's edges."""
 import numpy as np
@@ -23,7 +22,9 @@ def gpu():
 # rows and columns that end inside a slab (32 x 128), one group, rows a wave's share does not reach, more column tiles
 # than workgroups, more slabs down a tile than workgroups, segments that start in one chunk and end in the next
 SHAPES = [(8, 32), (8, 256), (40, 96), (32, 128), (256, 160), (1000, 288), (72, 70016), (9000, 64), (520, 5152),
-          (2056, 2080)]
+          (2056, 2080),
+          # rows that start inside a group: fewer columns than one, windows of 96 of 128 decoded ones
+          (8, 8), (48, 24), (40, 104), (1000, 296), (72, 70008), (9000, 72), (520, 5144), (2056, 2072)]
 
 
 def product(mat, d, m, add):
@@ -70,7 +71,7 @@ def test_outputs_aligned_to_their_elements_only(cols, m):
 
 
 @pytest.mark.parametrize("m", [3, 40])
-@pytest.mark.parametrize("rows,cols", [(40, 96), (200, 320)])
+@pytest.mark.parametrize("rows,cols", [(40, 96), (200, 320), (40, 88), (200, 328)])
 def test_infinities_and_nan_stay_in_their_columns(rows, cols, m):
     """Also in the last row, which the slab's rows past it repeat."""
     rng = rng_of(62, rows, m)
@@ -83,7 +84,8 @@ def test_infinities_and_nan_stay_in_their_columns(rows, cols, m):
 
 
 @pytest.mark.parametrize("m", [1, 20, 64])
-@pytest.mark.parametrize("rows,cols,pad", [(24, 64, 0), (333, 2080, 0), (704, 96, 8), (704, 96, 3)])
+@pytest.mark.parametrize("rows,cols,pad", [(24, 64, 0), (333, 2080, 0), (704, 96, 8), (704, 96, 3), (1, 8, 0),
+                                           (35, 40, 0), (333, 2072, 5), (704, 104, 8)])
 def test_both_matrices_of_a_gated_block(rows, cols, pad, m):
     """dx = dg Wg + du Wu from the dg and du that the call returns, whose BF16
     values are the product's operands: within the rounding of dx and of FP32
