@@ -352,20 +352,23 @@ __global__ __launch_bounds__(kMmThreads, 2) void afx_mm_kernel(const MmArgs p) {
         }
 }
 
-// One 32-token fragment of every wave of one of the rest's tiles, or a quarter
-// of it (kQ 4 or 1): the ranges' sums added in their order (the same bits on
-// every run), then the outputs.
+// One 32-token fragment of every wave of one of the rest's tiles (kQ 4), or a
+// quarter of it for 2 of the waves (kQ 1): the ranges' sums added in their
+// order (the same bits on every run), then the outputs.
+constexpr uint32_t join_threads(int q) { return q == 4 ? kMmThreads : kMmThreads / 4; }
+constexpr uint32_t join_parts(int q) { return q == 4 ? 1 : 16; }
 template <int BM, int kEpi, uint32_t kAct, int kQ>
-__global__ __launch_bounds__(kMmThreads) void afx_mm_join_kernel(const MmArgs p) {
-    constexpr uint32_t kMT = BM / 64, kParts = 4 / kQ;
-    const uint32_t q0 = blockIdx.x % kParts * kQ, j = blockIdx.x / kParts % kMT;
+__global__ __launch_bounds__(join_threads(kQ)) void afx_mm_join_kernel(const MmArgs p) {
+    constexpr uint32_t kMT = BM / 64, kParts = join_parts(kQ);
+    const uint32_t part = blockIdx.x % kParts, q0 = part % 4, j = blockIdx.x / kParts % kMT;
     const uint32_t mt = blockIdx.x / (kParts * kMT) % p.plan.m_tiles, nr = blockIdx.x / (kParts * kMT) / p.plan.m_tiles;
-    const uint32_t lane = threadIdx.x & (kMmWave - 1), wave = threadIdx.x / kMmWave;
+    const uint32_t thread = part / 4 * join_threads(kQ) + threadIdx.x;  // of the tile's workgroup
+    const uint32_t lane = thread & (kMmWave - 1), wave = thread / kMmWave;
     f32x4 acc[kQ][2] = {};
     const uint64_t range = (uint64_t)p.plan.m_tiles * (8 * kMT * kMmThreads);  // from one to the next
     const f32x4 *in = reinterpret_cast<const f32x4 *>(p.partial) + nr * p.plan.splits * range +
-                      (uint64_t)mt * (8 * kMT * kMmThreads) + (8 * j + 2 * q0) * kMmThreads + threadIdx.x;
-#pragma unroll(4 / kQ)
+                      (uint64_t)mt * (8 * kMT * kMmThreads) + (8 * j + 2 * q0) * kMmThreads + thread;
+#pragma unroll(8 / kQ)
     for (uint32_t s = 0; s < p.plan.splits; ++s)
 #pragma unroll
         for (int k = 0; k < 2 * kQ; ++k) acc[k / 2][k % 2] += in[s * range + k * kMmThreads];
@@ -441,13 +444,13 @@ int launch(MmArgs &p, hipStream_t stream) {
         return AFX_E_HIP;
     if (q.splits == 1) return AFX_OK;
     // Whole fragments write whole lines (64 tiles of 256 tokens, gated: 16 us,
-    // 23 in quarters); few of them leave CUs idle and are quartered (6 tiles
-    // of 64 tokens: 13.8 us, 4.3 in quarters).
+    // 23 in quarters); few of them leave CUs idle and are divided (6 tiles of
+    // 64 tokens, 32 ranges: 13.8 us, 4.6 divided).
     const uint32_t frags = q.n_rest * q.m_tiles * (BM / 64);
     const bool whole = frags >= 256;
     const void *join = whole ? reinterpret_cast<const void *>(&afx_mm_join_kernel<BM, kEpi, kAct, 4>)
                              : reinterpret_cast<const void *>(&afx_mm_join_kernel<BM, kEpi, kAct, 1>);
-    return hipLaunchKernel(join, dim3(whole ? frags : 4 * frags), dim3(kMmThreads), args, 0, stream) == hipSuccess
+    return hipLaunchKernel(join, dim3(frags * join_parts(whole ? 4 : 1)), dim3(join_threads(whole ? 4 : 1)), args, 0, stream) == hipSuccess
                ? AFX_OK
                : AFX_E_HIP;
 }

@@ -412,8 +412,12 @@ uint32_t norm_blocks(const NormShape &s, uint32_t m, uint32_t most) {
 }
 constexpr uint32_t kForwardBlocks = 8192;
 // Workgroups of the gradients' launch, each with its sums over its rows: one
-// or two on a CU.
-uint32_t grad_blocks(const NormShape &s, uint32_t m) { return norm_blocks(s, m, s.threads > 512 ? 256 : 512); }
+// on a CU from 10 waves on, more where they are small (4096 rows of 1024, 2
+// waves each: 37 us with 1024 workgroups, 44 with 512; of 500 values, 4 waves:
+// 20 and 18).
+uint32_t grad_blocks(const NormShape &s, uint32_t m) {
+    return norm_blocks(s, m, s.threads > 512 ? 256 : s.threads > 128 ? 512 : 1024);
+}
 
 template <bool kGrad, uint32_t kTeam, bool kVec, int I, uint32_t kThreads>
 const void *norm_kernel(bool fp32) {
