@@ -368,7 +368,8 @@ __global__ __launch_bounds__(join_threads(kQ)) void afx_mm_join_kernel(const MmA
     const uint64_t range = (uint64_t)p.plan.m_tiles * (8 * kMT * kMmThreads);  // from one to the next
     const f32x4 *in = reinterpret_cast<const f32x4 *>(p.partial) + nr * p.plan.splits * range +
                       (uint64_t)mt * (8 * kMT * kMmThreads) + (8 * j + 2 * q0) * kMmThreads + thread;
-#pragma unroll(8 / kQ)
+    constexpr int kAtOnce = 8 / kQ;  // ranges requested together
+#pragma unroll kAtOnce
     for (uint32_t s = 0; s < p.plan.splits; ++s)
 #pragma unroll
         for (int k = 0; k < 2 * kQ; ++k) acc[k / 2][k % 2] += in[s * range + k * kMmThreads];
