@@ -160,7 +160,7 @@ void afx_gated_gemm_kernel(const SlabArgs p) {
                 reinterpret_cast<const u32x4 *>(row + g.start + min(64 * i + 16 * c, g.len - 16)));
     };
     load_bits(tile, k0);
-    words = seg_words_of<4, kSegWords, kSegMaxStart>(bits);
+    words = seg_words_of<4, kSegWords, kSegMaxStart>(T, bits);
     load_words();
     load_bits(tile_n, k0_n);
     [[clang::always_inline]] build_lut<kWavesWG * kWave, true>(len, lds.plut, lds.scratch);
@@ -192,7 +192,7 @@ void afx_gated_gemm_kernel(const SlabArgs p) {
         // sign/mantissa bytes, the next slab's words, the one after's offsets.
         load_sm(tile, k0);
         if (s + 1 < s1) {
-            words = seg_words_of<4, kSegWords, kSegMaxStart>(bits);
+            words = seg_words_of<4, kSegWords, kSegMaxStart>(T, bits);
             load_words();
         }
         if (s + 2 < s1) {

@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kWavesWG *kWave, kWavesWG / 4) void afx_gemm_t_kern
     At cur = settle(At{tile0, s0 - tile0 * blocks + wr}), nxt = cur;
     if (there(cur)) {
         load_bits(cur);
-        words = seg_words_of<2, kRowWords, kRowMaxStart>(bits);
+        words = seg_words_of<2, kRowWords, kRowMaxStart>(T, bits);
         load_words();
         nxt = next(cur);
         if (there(nxt)) load_bits(nxt);
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kWavesWG *kWave, kWavesWG / 4) void afx_gemm_t_kern
             load_sm(cur);
             const At aft = there(nxt) ? next(nxt) : nxt;
             if (there(nxt)) {
-                words = seg_words_of<2, kRowWords, kRowMaxStart>(bits);
+                words = seg_words_of<2, kRowWords, kRowMaxStart>(T, bits);
                 load_words();
             }
             if (there(aft)) load_bits(aft);

@@ -152,6 +152,44 @@ constexpr uint32_t seg_chain_r0(uint64_t p, uint64_t wa) {
     return 32 * kSegRev - (uint32_t)umin64(p - 32 * wa, kSegMaxStart);
 }
 
+// ---- row segments relative to a tile (afx_segments.h) -------------------------
+// A segment is len elements (whole groups, at most 256) from `start` on, and
+// `left` elements remain to the tensor's end, all counted from a tile's first
+// element (the start of a group), which is element in_chunk of its chunk. It
+// ends in the chunk that it starts in, or in the next.
+constexpr uint32_t kSegLast = 8;  // SegRefs::next: the segment ends the tensor
+struct SegRefs {
+    uint32_t chunk;    // the chunk that the segment starts in, from the tile's
+    uint32_t a, b, e;  // gaps, from the tile's first: of its groups 2 c and 2 c + 1, and of the group after it
+    uint32_t next;     // bits 0, 1, 2: whether those groups lie in the chunk after `chunk`; kSegLast
+};
+// (A group past the segment's end repeats its last one: decoded, not used.)
+constexpr SegRefs seg_refs(uint32_t in_chunk, uint32_t left, uint32_t start, uint32_t len, uint32_t c) {
+    const uint32_t at = in_chunk + start, ch = at / kChunk, most = len / kGroup - 1, end = start + len;
+    const uint32_t ga = umin32(2 * c, most), gb = umin32(2 * c + 1, most);
+    const bool last = end >= left;
+    SegRefs r{};
+    r.chunk = ch;
+    r.a = start / kGroup + ga;
+    r.b = start / kGroup + gb;
+    r.e = last ? 0 : end / kGroup;
+    r.next = ((at + kGroup * ga) / kChunk - ch) | ((at + kGroup * gb) / kChunk - ch) << 1 |
+             (last ? kSegLast : ((in_chunk + end) / kChunk - ch) << 2);
+    return r;
+}
+// The bit where the segment ends, modulo 2^32: that of the group after it
+// (base0, base1: bit bases of `chunk` and the one after; gap: the group's), or
+// the stream's end. (The last segment may end in the chunk after `chunk`, so
+// neither base tells the stream's end.)
+constexpr uint32_t seg_end(uint32_t next, uint32_t base0, uint32_t base1, uint32_t gap, uint32_t stream_bits) {
+    return next & kSegLast ? stream_bits : (next & 4 ? base1 : base0) + gap;
+}
+// Words to stage from stream word wa through that bit, plus one of look-ahead;
+// at most `most`, whatever a corrupt stream says.
+constexpr uint32_t seg_staged(uint32_t end, uint64_t wa, uint32_t most) {
+    return umin32(((end - ((uint32_t)wa << 5) + 31) >> 5) + 1, most);
+}
+
 // ---- the MFMA product's launch order ----------------------------------------
 // Not derived from blob contents, but checked with the rest: block b of a
 // launch with nt token blocks per tile takes tile gemm_block_tile(b, nt) (at

@@ -42,27 +42,21 @@ struct Seg {
 };
 
 // What the bit offsets of the lane's groups 2 c and 2 c + 1 of a segment and
-// of its end are made of, kept as loaded and added up only where used. (A
-// segment lies in one chunk or ends in the next; a group past the row's end
-// repeats the row's last one: it is decoded, not used.)
+// of its end are made of (afx_index.h), kept as loaded and added up only
+// where used.
 struct Bits {
-    u32x4 base;      // u64 bit bases of the chunk that the segment starts in, and of the next
+    u32x4 base;        // u64 bit bases of the chunk that the segment starts in, and of the next
     uint32_t a, b, e;  // gaps of the lane's groups and of the group after the segment
-    uint32_t next;     // bits 0, 1, 2: whether each is in the next chunk; bit 3: the segment ends the
-                       // tensor (the stream's end, with no gap)
+    uint32_t next;     // SegRefs::next
 };
 __device__ inline Bits seg_bits(const Tile &t, const Seg &g, uint32_t c) {
+    const SegRefs r = seg_refs(t.in_chunk, t.left, g.start, g.len, c);
     Bits b;
-    const uint32_t ch = (t.in_chunk + g.start) >> 12, most = g.len / kGroup - 1, end = g.start + g.len;
-    const uint32_t ga = min(2 * c, most), gb = min(2 * c + 1, most);
-    __builtin_memcpy(&b.base, t.base + ch, 16);  // (8-byte aligned; the entry after the last chunk's exists)
-    const bool last = end >= t.left;
-    b.a = t.gap[(g.start >> 5) + ga];
-    b.b = t.gap[(g.start >> 5) + gb];
-    b.e = t.gap[last ? 0 : end >> 5];
-    // (chunks ch and ch + 1 only: the difference is 0 or 1)
-    b.next = (((t.in_chunk + g.start + kGroup * ga) >> 12) - ch) | (((t.in_chunk + g.start + kGroup * gb) >> 12) - ch) << 1 |
-             (last ? 12u : (((t.in_chunk + end) >> 12) - ch) << 2);
+    __builtin_memcpy(&b.base, t.base + r.chunk, 16);  // (8-byte aligned; the entry after the last chunk's exists)
+    b.a = t.gap[r.a];
+    b.b = t.gap[r.b];
+    b.e = t.gap[r.e];
+    b.next = r.next;
     return b;
 }
 
@@ -74,19 +68,20 @@ struct Words {
     uint32_t nw, starts;
 };
 template <int kParts, uint32_t kWords, uint32_t kMaxStart>
-__device__ inline Words seg_words_of(const Bits &b) {
+__device__ inline Words seg_words_of(const TensorDesc &T, const Bits &b) {
     const uint64_t b0 = ((uint64_t)b.base.y << 32) | b.base.x, bn = ((uint64_t)b.base.w << 32) | b.base.z;
     const uint64_t pa = (b.next & 1 ? bn : b0) + b.a;
     Words w;
     w.wa = seg_first_word(row_first<kParts>(pa));
     const uint32_t first = (uint32_t)w.wa << 5;
-    w.nw = min((((b.next & 4 ? b.base.z : b.base.x) + (b.next & 8 ? 0u : b.e) - first + 31) >> 5) + 1, kWords);
+    w.nw = seg_staged(seg_end(b.next, b.base.x, b.base.z, b.e, T.reserved), w.wa, kWords);
     w.starts = min((uint32_t)pa - first, kMaxStart) |
                min((b.next & 2 ? b.base.z : b.base.x) + b.b - first, kMaxStart) << 16;
     static_assert(kMaxStart < 1u << 16, "a start fits 16 bits");
     return w;
 }
 
+// (`reserved`: the stream's length in bits, modulo 2^32)
 inline TensorDesc tensor(const afx_info *info, const void *blob) {
     const uint8_t *b = static_cast<const uint8_t *>(blob);
     TensorDesc t{};
@@ -99,6 +94,7 @@ inline TensorDesc tensor(const afx_info *info, const void *blob) {
     t.exp_words = info->exp_words;
     t.last_word4 = last_word4(info->exp_words);
     t.n_chunks = (uint32_t)info->n_chunks;
+    t.reserved = (uint32_t)info->total_bits;
     return t;
 }
 
