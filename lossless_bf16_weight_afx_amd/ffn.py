@@ -53,8 +53,9 @@ class FeedForward:
         new = lambda n, t=torch.bfloat16: torch.empty((max_tokens, n), dtype=t, device=dev)  # noqa: E731
         self.xn, self.h, self.b, self.r_out = new(d), new(ff), new(d, torch.float32), new(d)
         self.xn_next = new(d) if w_next is not None else None
-        # A workspace's size need not grow with the tokens (other kernels, other divisions of the work), but it does
-        # within a tile of tokens: the largest is at one of these.
+        # A workspace's size need not grow with the tokens: up to 128 of them other kernels take over, and from there
+        # on the division of the work follows from how many tiles of 64, 128 and 256 tokens there are. It does grow
+        # while the number of tiles of 64 stays, so the largest is at one of these.
         sizes = [afx.afx_restore_gated_workspace(ff, d, m) for m in self._sizes()]
         self.training = training
         if training:
@@ -70,7 +71,7 @@ class FeedForward:
 
     def _sizes(self):
         n = self.max_tokens
-        return sorted({*range(1, min(n, 256) + 1), *range(256, n + 1, 256), n})
+        return sorted({*range(1, min(n, 256) + 1), *range(256, n + 1, 64), n})
 
     def _stream(self, m: int) -> int:
         import torch
