@@ -16,7 +16,9 @@ gradients.
 
 This module only holds buffers and makes calls: everything is enqueued on the
 current stream, which a HIP graph may capture, and nothing is allocated after
-the constructor. One object serves one stream at a time.
+the constructor. One object serves one stream at a time, and with
+training=True a forward() and its backward() take turns: backward() needs
+what forward() kept, and writes over it.
 """
 from __future__ import annotations
 
@@ -58,6 +60,8 @@ class FeedForward:
         # while the number of tiles of 64 stays, so the largest is at one of these.
         sizes = [afx.afx_restore_gated_workspace(ff, d, m) for m in self._sizes()]
         self.training = training
+        self._kept = None  # training: the stream (address, stride, tokens) of the forward pass whose values are held
+        self._captured = False  # whether that pass was captured into a graph
         if training:
             self.g, self.u, self.db, self.dxn, self.dr = new(ff), new(ff), new(d), new(d), new(d)
             self.dh = new(ff, torch.float32)
@@ -88,11 +92,27 @@ class FeedForward:
             raise ValueError(f"a residual stream is a BF16 [tokens, {self.d}] tensor on {self.ws.device}, rows whole")
         return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else self.d  # (one row's stride may be anything)
 
+    def _own(self, ptr: int, ld: int, m: int) -> bool:
+        """Whether rows of a stream share memory with this object's buffers."""
+        end = ptr + 2 * ((m - 1) * ld + self.d)
+        own = (self.xn, self.h, self.b, self.r_out, self.xn_next, self.g, self.u, self.db, self.dxn, self.dr, self.dh,
+               self.ws)
+        return any(t is not None and ptr < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < end
+                   for t in own)
+
     def forward(self, r):
         """r' and xn' (None without w_next) for the residual stream r, in this
-        object's buffers (views of its first rows)."""
+        object's buffers (views of its first rows). Without training r may be
+        r' of the last pass itself; with it r is read once more by backward()
+        and may not lie in this object's buffers."""
+        import torch
+
         m, (r_ptr, ld) = r.shape[0], self._residual(r)
         s, d, ff = self._stream(m), self.d, self.ff
+        if self.training:
+            if self._own(r_ptr, ld, m):
+                raise ValueError("the residual stream lies in this object's buffers, which backward() would need")
+            self._kept, self._captured = None, torch.cuda.is_current_stream_capturing()
         g, u = (self.g.data_ptr(), self.u.data_ptr()) if self.training else (0, 0)
         xn_next = 0 if self.xn_next is None else self.xn_next.data_ptr()
         afx.afx_block_norm_async(self.norm_in, m, 0, 0, r_ptr, ld, 0, 0, self.xn.data_ptr(), d, s)
@@ -103,11 +123,18 @@ class FeedForward:
                                    self.b.data_ptr(), s)
         afx.afx_block_norm_async(self.norm_out, m, self.b.data_ptr(), d, r_ptr, ld, self.r_out.data_ptr(), d, xn_next,
                                  d, s)
+        if self.training:
+            self._kept = (r_ptr, ld, m)
         return self.r_out[:m], None if self.xn_next is None else self.xn_next[:m]
 
     def backward(self, r, dr_out, dxn_next=None):
-        """dr, the gradient of r, from those of r' and xn', after forward(r).
-        dw_pre, dw_post, dgate and dw_next hold the vectors' gradients."""
+        """dr, the gradient of r, from those of r' and xn', once after each
+        forward(r), with the same r. dw_pre, dw_post, dgate and dw_next hold
+        the vectors' gradients. (If a graph captured that pass, its replays
+        are not seen here: they are taken to come before each backward() that
+        is not captured.)"""
+        import torch
+
         if not self.training:
             raise ValueError("the object was made without training=True")
         m, (r_ptr, ld), (dro, ld_dro) = r.shape[0], self._residual(r), self._residual(dr_out)
@@ -115,12 +142,17 @@ class FeedForward:
         if dr_out.shape[0] != m or (dxn_next is not None and (dxn_next.shape[0] != m or self.xn_next is None)):
             raise ValueError("the gradients do not match the forward pass")
         s, d, ff, ws, n = self._stream(m), self.d, self.ff, self.ws.data_ptr(), self.ws.numel()
+        if self._kept != (r_ptr, ld, m):
+            raise ValueError("each backward() follows a forward() of its own" if self._kept is None else
+                             "r is not the stream of the last forward pass")
         addr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
         afx.afx_block_norm_backward_async(self.norm_out, m, self.b.data_ptr(), d, self.r_out.data_ptr(), d, dxo,
                                           ld_dxo, dro, ld_dro, self.dr.data_ptr(), d, self.db.data_ptr(), d,
                                           addr(self.dw_next), addr(self.dw_post), addr(self.dgate), ws, n, s)
         afx.afx_restore_gemm_t_async(self.down[0], self.down[1].data_ptr(), d, ff, self.db.data_ptr(), m,
                                      self.dh.data_ptr(), False, ws, n, s)
+        if not self._captured or torch.cuda.is_current_stream_capturing():
+            self._kept = None
         # dg and du take the places of g and u: with xn they give the gradients of the two matrices' products
         afx.afx_restore_gated_backward_async(self.weights, m, self.dh.data_ptr(), ff, self.g.data_ptr(),
                                              self.u.data_ptr(), ff, self.dxn.data_ptr(), d, self.g.data_ptr(),

@@ -38,3 +38,97 @@ def test_workspace_holds_every_token_count(d, ff, max_tokens, training):
                        afx.afx_restore_gemm_t_workspace(d, ff, m), afx.afx_block_norm_workspace(t.norm_in, m),
                        afx.afx_block_norm_workspace(t.norm_out, m))
     assert t.ws.numel() == max(need, 16)
+
+
+# ---------------------------------------------------------------------------
+# what the buffers hold between forward() and backward()
+# ---------------------------------------------------------------------------
+CALLS = ("afx_block_norm_async", "afx_restore_gated_async", "afx_restore_gemm_async", "afx_block_norm_backward_async",
+         "afx_restore_gemm_t_async", "afx_restore_gated_backward_async")
+
+
+class Stream:
+    cuda_stream = 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The names of the library's calls, in order; `capturing` as a graph's capture would have it."""
+    made = []
+    for name in CALLS:
+        monkeypatch.setattr(afx, name, lambda *a, name=name: made.append(name))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return made
+
+
+def values(m, d=64):
+    return torch.ones(m, d, dtype=torch.bfloat16)
+
+
+def refused(calls, f, *args):
+    """ValueError, and nothing was called."""
+    n = len(calls)
+    with pytest.raises(ValueError):
+        f(*args)
+    assert len(calls) == n
+
+
+def test_backward_takes_the_kept_values_once(calls):
+    """dg and du take the places of g and u: a second backward() would take
+    them for g and u."""
+    t, r = block(64, 256, 8, True), values(8)
+    refused(calls, t.backward, r, r)  # no forward pass yet
+    t.forward(r)
+    t.backward(r, r)
+    refused(calls, t.backward, r, r)
+    t.forward(r)
+    refused(calls, t.backward, r, values(7))  # refused arguments leave the kept values
+    t.backward(r, r)
+    assert calls == (list(CALLS[:3]) + [CALLS[0]] + list(CALLS[3:]) + [CALLS[3]]) * 2
+
+
+def test_backward_is_of_the_last_forward_pass(calls):
+    t, r, wide = block(64, 256, 8, True), values(8), torch.ones(8, 128, dtype=torch.bfloat16)
+    t.forward(r)
+    for other in (values(8), r[:5], r[1:], wide[:, :64]):
+        refused(calls, t.backward, other, values(other.shape[0]))
+    t.backward(r[:], values(8))  # a view of the same rows
+    t.forward(wide[:, 64:])
+    refused(calls, t.backward, wide[:, :64], r)
+    t.forward(r[2:3])
+    refused(calls, t.backward, r[:1], r[:1])
+    t.backward(r[2:3], r[:1])
+
+
+def test_training_does_not_overwrite_the_stream(calls):
+    """backward() reads r once more: it may not lie in the object's own buffers."""
+    w = torch.ones(64, dtype=torch.bfloat16)
+    t, r = block(64, 256, 8, True, w_next=w), values(8)
+    t.forward(r)
+    for own in (t.r_out, t.r_out[2:5], t.xn, t.xn_next, t.h[:, :64], t.g[:, 64:128], t.u[:3, :64], t.db, t.dxn, t.dr):
+        refused(calls, t.forward, own)
+    t.backward(r, r)  # what the last forward pass kept is still there
+    other = block(64, 256, 8)
+    ro, _ = other.forward(r)
+    other.forward(ro)  # without training, in place
+    t.forward(ro)  # another object's output
+    t.backward(ro, t.dr)
+
+
+def test_a_captured_forward_pass_may_be_replayed_between_backward_calls(calls, monkeypatch):
+    """Replays are not seen here, so what they keep is taken to be there;
+    not so after a graph of both passes."""
+    t, r = block(64, 256, 8, True), values(8)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    t.forward(r)
+    t.backward(r, r)
+    refused(calls, t.backward, r, r)
+    t.forward(r)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    t.backward(r, r)
+    t.backward(r, r)
+    refused(calls, t.backward, values(8), r)
+    t.forward(r)
+    t.backward(r, r)
+    refused(calls, t.backward, r, r)
