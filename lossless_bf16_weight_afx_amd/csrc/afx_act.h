@@ -23,7 +23,9 @@ __device__ inline float act(float g) {
 }
 
 // act(g) and act'(g). SiLU: s (1 + g (1 - s)); tanh form: with s =
-// sigmoid(2z), s + g s (1 - s) 2 z'; GELU: cdf + g pdf.
+// sigmoid(2z), s + g s (1 - s) 2 z'; GELU: cdf + g pdf. In the tanh form z'
+// is taken at |g| <= 16, where 1 - s or s is 0 already (2z = 318): its square
+// would overflow from |g| = 1.8e19 on, and infinity times 0 is NaN.
 template <uint32_t kAct>
 __device__ inline void act_grad(float g, float &a, float &da) {
     if constexpr (kAct == AFX_ACT_SILU) {
@@ -33,7 +35,8 @@ __device__ inline void act_grad(float g, float &a, float &da) {
     } else if constexpr (kAct == AFX_ACT_GELU_TANH) {
         const float s = sigmoid(2.f * kGeluC * (g + kGeluA * g * g * g));
         a = act<kAct>(g);
-        da = s + g * s * (1.f - s) * (2.f * kGeluC) * (1.f + 3.f * kGeluA * g * g);
+        const float t = fminf(fmaxf(g, -16.f), 16.f);
+        da = s + t * s * (1.f - s) * (2.f * kGeluC) * (1.f + 3.f * kGeluA * t * t);
     } else {
         const float cdf = 0.5f * erfcf(-0.7071067811865476f * g);
         a = g * cdf;
