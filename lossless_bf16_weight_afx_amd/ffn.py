@@ -28,8 +28,9 @@ from . import afx
 class FeedForward:
     """gate, up: (info, device blob) of [ff, d] matrices; down: of a [d, ff]
     one (d a multiple of 64, ff of 256). Norm weights and a gate are BF16
-    device tensors [d]; w_post, block_gate and w_next may be None. Buffers
-    are for up to max_tokens tokens; training keeps what backward() needs."""
+    device tensors [d]; w_post, block_gate and w_next may be None. All are on
+    one device, where the calls run whichever device is current. Buffers are
+    for up to max_tokens tokens; training keeps what backward() needs."""
 
     def __init__(self, gate, up, down, d: int, ff: int, w_pre, *, w_post=None, block_gate=None, w_next=None,
                  act: int = afx.ACT_SILU, eps: float = 1e-6, scale: float = 1.0, max_tokens: int, training=False):
@@ -37,8 +38,12 @@ class FeedForward:
 
         if d % 64 or ff % 256 or d < 64 or ff < 256:
             raise ValueError(f"d {d} and ff {ff}: the down product takes multiples of 64 and 256")
-        if any(int(info.n_elems) != d * ff for info, _ in (gate, up, down)):
-            raise ValueError(f"a matrix does not have {d} x {ff} values")
+        for (info, blob), shape in ((gate, (ff, d)), (up, (ff, d)), (down, (d, ff))):
+            # (coded with another number of dimensions, the values are taken in order)
+            if int(info.n_elems) != d * ff or (info.ndim == 2 and tuple(info.shape[:2]) != shape):
+                raise ValueError(f"a matrix is not one of {shape[0]} x {shape[1]} values")
+            if blob.device != w_pre.device:
+                raise ValueError("the matrices and the norm weights are on one device")
         if max_tokens < 1:
             raise ValueError("max_tokens must be at least 1")
         for t in (w_pre, w_post, block_gate, w_next):
@@ -109,20 +114,21 @@ class FeedForward:
 
         m, (r_ptr, ld) = r.shape[0], self._residual(r)
         s, d, ff = self._stream(m), self.d, self.ff
-        if self.training:
-            if self._own(r_ptr, ld, m):
-                raise ValueError("the residual stream lies in this object's buffers, which backward() would need")
-            self._kept, self._captured = None, torch.cuda.is_current_stream_capturing()
+        if self.training and self._own(r_ptr, ld, m):
+            raise ValueError("the residual stream lies in this object's buffers, which backward() would need")
         g, u = (self.g.data_ptr(), self.u.data_ptr()) if self.training else (0, 0)
         xn_next = 0 if self.xn_next is None else self.xn_next.data_ptr()
-        afx.afx_block_norm_async(self.norm_in, m, 0, 0, r_ptr, ld, 0, 0, self.xn.data_ptr(), d, s)
-        afx.afx_restore_gated_async(self.weights, m, self.xn.data_ptr(), d, self.h.data_ptr(), ff, g, u, ff,
-                                    self.ws.data_ptr(), self.ws.numel(), s)
-        self.b[:m].zero_()
-        afx.afx_restore_gemm_async(self.down[0], self.down[1].data_ptr(), d, ff, self.h.data_ptr(), m,
-                                   self.b.data_ptr(), s)
-        afx.afx_block_norm_async(self.norm_out, m, self.b.data_ptr(), d, r_ptr, ld, self.r_out.data_ptr(), d, xn_next,
-                                 d, s)
+        with torch.cuda.device(self.ws.device):
+            if self.training:
+                self._kept, self._captured = None, torch.cuda.is_current_stream_capturing()
+            afx.afx_block_norm_async(self.norm_in, m, 0, 0, r_ptr, ld, 0, 0, self.xn.data_ptr(), d, s)
+            afx.afx_restore_gated_async(self.weights, m, self.xn.data_ptr(), d, self.h.data_ptr(), ff, g, u, ff,
+                                        self.ws.data_ptr(), self.ws.numel(), s)
+            self.b[:m].zero_()
+            afx.afx_restore_gemm_async(self.down[0], self.down[1].data_ptr(), d, ff, self.h.data_ptr(), m,
+                                       self.b.data_ptr(), s)
+            afx.afx_block_norm_async(self.norm_out, m, self.b.data_ptr(), d, r_ptr, ld, self.r_out.data_ptr(), d,
+                                     xn_next, d, s)
         if self.training:
             self._kept = (r_ptr, ld, m)
         return self.r_out[:m], None if self.xn_next is None else self.xn_next[:m]
@@ -146,18 +152,19 @@ class FeedForward:
             raise ValueError("each backward() follows a forward() of its own" if self._kept is None else
                              "r is not the stream of the last forward pass")
         addr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-        afx.afx_block_norm_backward_async(self.norm_out, m, self.b.data_ptr(), d, self.r_out.data_ptr(), d, dxo,
-                                          ld_dxo, dro, ld_dro, self.dr.data_ptr(), d, self.db.data_ptr(), d,
-                                          addr(self.dw_next), addr(self.dw_post), addr(self.dgate), ws, n, s)
-        afx.afx_restore_gemm_t_async(self.down[0], self.down[1].data_ptr(), d, ff, self.db.data_ptr(), m,
-                                     self.dh.data_ptr(), False, ws, n, s)
-        if not self._captured or torch.cuda.is_current_stream_capturing():
-            self._kept = None
-        # dg and du take the places of g and u: with xn they give the gradients of the two matrices' products
-        afx.afx_restore_gated_backward_async(self.weights, m, self.dh.data_ptr(), ff, self.g.data_ptr(),
-                                             self.u.data_ptr(), ff, self.dxn.data_ptr(), d, self.g.data_ptr(),
-                                             self.u.data_ptr(), ws, n, s)
-        afx.afx_block_norm_backward_async(self.norm_in, m, 0, 0, r_ptr, ld, self.dxn.data_ptr(), d,
-                                          self.dr.data_ptr(), d, self.dr.data_ptr(), d, 0, 0, addr(self.dw_pre), 0, 0,
-                                          ws, n, s)
+        with torch.cuda.device(self.ws.device):
+            afx.afx_block_norm_backward_async(self.norm_out, m, self.b.data_ptr(), d, self.r_out.data_ptr(), d, dxo,
+                                              ld_dxo, dro, ld_dro, self.dr.data_ptr(), d, self.db.data_ptr(), d,
+                                              addr(self.dw_next), addr(self.dw_post), addr(self.dgate), ws, n, s)
+            afx.afx_restore_gemm_t_async(self.down[0], self.down[1].data_ptr(), d, ff, self.db.data_ptr(), m,
+                                         self.dh.data_ptr(), False, ws, n, s)
+            if not self._captured or torch.cuda.is_current_stream_capturing():
+                self._kept = None
+            # dg and du take the places of g and u: with xn they give the gradients of the two matrices' products
+            afx.afx_restore_gated_backward_async(self.weights, m, self.dh.data_ptr(), ff, self.g.data_ptr(),
+                                                 self.u.data_ptr(), ff, self.dxn.data_ptr(), d, self.g.data_ptr(),
+                                                 self.u.data_ptr(), ws, n, s)
+            afx.afx_block_norm_backward_async(self.norm_in, m, 0, 0, r_ptr, ld, self.dxn.data_ptr(), d,
+                                              self.dr.data_ptr(), d, self.dr.data_ptr(), d, 0, 0, addr(self.dw_pre), 0,
+                                              0, ws, n, s)
         return self.dr[:m]

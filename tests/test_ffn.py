@@ -1,5 +1,7 @@
 """ffn.FeedForward's own part (buffers, checks, order of calls) on the CPU:
 the library's calls that would run on the GPU are recorded instead."""
+import contextlib
+
 import pytest
 
 from lossless_bf16_weight_afx_amd import afx, ffn
@@ -59,6 +61,7 @@ def calls(monkeypatch):
         monkeypatch.setattr(afx, name, lambda *a, name=name: made.append(name))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "device", contextlib.nullcontext)
     return made
 
 
@@ -132,3 +135,49 @@ def test_a_captured_forward_pass_may_be_replayed_between_backward_calls(calls, m
     t.forward(r)
     t.backward(r, r)
     refused(calls, t.backward, r, r)
+
+
+# ---------------------------------------------------------------------------
+# matrices and devices
+# ---------------------------------------------------------------------------
+def test_matrices_of_another_shape_are_refused():
+    d, ff, w, blob = 64, 256, torch.ones(64, dtype=torch.bfloat16), torch.zeros(16, dtype=torch.uint8)
+    gate, up, down = matrices(d, ff)
+    for bad in ([(info(d, ff), blob), up, down], [gate, (info(128, 128), blob), down], [gate, up, (info(ff, d), blob)],
+                [gate, up, (info(d, 2 * ff), blob)]):
+        with pytest.raises(ValueError):
+            ffn.FeedForward(*bad, d, ff, w, max_tokens=4)
+    flat = info(d, ff)  # coded without a shape of two dimensions: taken as the matrix, as the library's calls do
+    flat.ndim, flat.shape[0], flat.shape[1] = 1, d * ff, 0
+    ffn.FeedForward(gate, up, (flat, blob), d, ff, w, max_tokens=4)
+
+
+def test_matrices_on_another_device_are_refused():
+    gate, up, down = matrices(64, 256)
+    away = torch.zeros(16, dtype=torch.uint8, device="meta")
+    for bad in ([(gate[0], away), up, down], [gate, (up[0], away), down], [gate, up, (down[0], away)]):
+        with pytest.raises(ValueError):
+            ffn.FeedForward(*bad, 64, 256, torch.ones(64, dtype=torch.bfloat16), max_tokens=4)
+
+
+def test_calls_run_on_the_buffers_device(calls, monkeypatch):
+    """Whichever device is current: a default stream is the current device's."""
+    current = []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for name in CALLS:
+        monkeypatch.setattr(afx, name, lambda *a, name=name: calls.append((name, list(current))))
+    t, r = block(64, 256, 8, True), values(8)
+    t.forward(r)
+    t.backward(r, r)
+    assert len(calls) == 8 and all(on == [t.ws.device] for _, on in calls) and not current
