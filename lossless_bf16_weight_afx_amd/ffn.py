@@ -98,24 +98,25 @@ class FeedForward:
         return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else self.d  # (one row's stride may be anything)
 
     def _own(self, ptr: int, ld: int, m: int) -> bool:
-        """Whether rows of a stream share memory with this object's buffers."""
+        """Whether rows of a stream lie in buffers that the passes write before they have read them: all, but r'
+        without training."""
         end = ptr + 2 * ((m - 1) * ld + self.d)
-        own = (self.xn, self.h, self.b, self.r_out, self.xn_next, self.g, self.u, self.db, self.dxn, self.dr, self.dh,
-               self.ws)
+        own = [self.xn, self.h, self.b, self.xn_next, self.ws]
+        if self.training:
+            own += [self.r_out, self.g, self.u, self.db, self.dxn, self.dr, self.dh]
         return any(t is not None and ptr < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < end
                    for t in own)
 
     def forward(self, r):
         """r' and xn' (None without w_next) for the residual stream r, in this
-        object's buffers (views of its first rows). Without training r may be
-        r' of the last pass itself; with it r is read once more by backward()
-        and may not lie in this object's buffers."""
+        object's buffers (views of its first rows). r may not lie in them, but
+        for r' of the last pass, without training (backward() reads r again)."""
         import torch
 
         m, (r_ptr, ld) = r.shape[0], self._residual(r)
         s, d, ff = self._stream(m), self.d, self.ff
-        if self.training and self._own(r_ptr, ld, m):
-            raise ValueError("the residual stream lies in this object's buffers, which backward() would need")
+        if self._own(r_ptr, ld, m):
+            raise ValueError("the residual stream lies in buffers that this object writes before it has read them")
         g, u = (self.g.data_ptr(), self.u.data_ptr()) if self.training else (0, 0)
         xn_next = 0 if self.xn_next is None else self.xn_next.data_ptr()
         with torch.cuda.device(self.ws.device):

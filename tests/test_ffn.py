@@ -181,3 +181,13 @@ def test_calls_run_on_the_buffers_device(calls, monkeypatch):
     t.forward(r)
     t.backward(r, r)
     assert len(calls) == 8 and all(on == [t.ws.device] for _, on in calls) and not current
+
+
+def test_a_stream_in_the_buffers_is_refused_without_training_too(calls):
+    """The gated block would write over it before the residual is added; only
+    r' itself may be the next pass's stream."""
+    t, r = block(64, 256, 8, w_next=torch.ones(64, dtype=torch.bfloat16)), values(8)
+    ro, xn = t.forward(r)
+    for own in (t.h[:, :64], t.h[:3, 64:128], t.xn, xn):
+        refused(calls, t.forward, own)
+    t.forward(ro)
