@@ -246,7 +246,10 @@ int afx_restore_gemm_batch_async(const afx_gemv_job *jobs, size_t n_jobs, uint32
  * and for the norms' own (uncoded) weights and gates. All buffers are device
  * memory owned by the caller; a workspace holds nothing between calls, and
  * calls that may run at the same time (two streams, two captured graphs)
- * each need their own. Strides count elements between rows (tokens). */
+ * each need their own. Strides count elements between rows (tokens). Buffers
+ * that may not share a byte may be column ranges of one wider matrix (rows
+ * the same number of bytes apart); of buffers with other row distances whole
+ * extents are compared, from the first byte to the last. */
 
 typedef enum afx_act {
     AFX_ACT_SILU = 0,      /* g / (1 + e^-g) */
@@ -381,8 +384,9 @@ int afx_block_norm_workspace(const afx_block_norm *p, uint32_t m, size_t *bytes)
  * Each output may be NULL (not computed). dr_dev may be dr_out_dev itself
  * with the same stride. dr is used unrounded in the others. b_dev NULL: only
  * dr and dw_pre. The sums over rows are FP32 and their order depends on the
- * sizes only: the same bits on every run; with m == 0 they are written as
- * zeros. Errors: as afx_block_norm_async (asking for dw_pre without w_pre,
+ * sizes only (that of the sums within a row, here and in the forward call,
+ * also on whether d, strides and alignment allow 8 values at a time): the
+ * same bits on every run; with m == 0 they are written as zeros. Errors: as afx_block_norm_async (asking for dw_pre without w_pre,
  * dw_post without w_post, dgate without gate, or db, dw_post or dgate
  * without b is AFX_E_INVALID_ARG); AFX_E_BUFFER_TOO_SMALL (workspace),
  * AFX_E_MISALIGNED also for a workspace not 16-byte aligned. */

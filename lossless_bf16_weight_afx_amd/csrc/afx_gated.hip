@@ -108,21 +108,18 @@ int launch_grad(const GradArgs &p, uint32_t act, hipStream_t stream) {
 }
 
 // ---- argument checks ---------------------------------------------------------
-// One caller buffer: `bytes` from p.
-struct Span {
-    const void *p;
-    uint64_t bytes;
-};
-Span span(const void *p, uint32_t m, uint64_t stride, uint64_t width, uint64_t elem) {
-    return Span{p, p && m ? ((uint64_t)(m - 1) * stride + width) * elem : 0};
+// A caller's buffer: m rows of `width` elements; or `bytes` in one piece.
+RowSpan span(const void *p, uint32_t m, uint64_t stride, uint64_t width, uint64_t elem) {
+    return RowSpan{p, m, width * elem, stride * elem};
 }
-bool any_overlap(const Span *a, size_t na, const Span *b, size_t nb) {
+RowSpan piece(const void *p, uint64_t bytes) { return RowSpan{p, bytes ? 1u : 0u, bytes, bytes}; }
+bool any_overlap(const RowSpan *a, size_t na, const RowSpan *b, size_t nb) {
     for (size_t i = 0; i < na; ++i)
         for (size_t k = 0; k < nb; ++k)
-            if (ranges_overlap(a[i].p, a[i].bytes, b[k].p, b[k].bytes)) return true;
+            if (rows_overlap(a[i], b[k])) return true;
     return false;
 }
-bool pairs_overlap(const Span *a, size_t n) {
+bool pairs_overlap(const RowSpan *a, size_t n) {
     for (size_t i = 0; i < n; ++i)
         if (any_overlap(a + i, 1, a + i + 1, n - i - 1)) return true;
     return false;
@@ -236,11 +233,11 @@ int afx_restore_gated_async(const afx_gated *w, uint32_t m, const uint16_t *x_de
         misaligned(u_dev, 2))
         return AFX_E_MISALIGNED;
     if (ws_bytes < sp.bytes) return AFX_E_BUFFER_TOO_SMALL;
-    const Span in[] = {{w->gate_blob_dev, w->gate_info->blob_bytes},
-                       {w->up_blob_dev, w->up_info->blob_bytes},
-                       span(x_dev, m, x_stride, w->cols, 2)};
-    const Span out[] = {span(h_dev, m, h_stride, w->rows, 2), span(g_dev, m, gu_stride, w->rows, 2),
-                        span(u_dev, m, gu_stride, w->rows, 2), {ws_dev, sp.bytes}};
+    const RowSpan in[] = {piece(w->gate_blob_dev, w->gate_info->blob_bytes),
+                          piece(w->up_blob_dev, w->up_info->blob_bytes),
+                          span(x_dev, m, x_stride, w->cols, 2)};
+    const RowSpan out[] = {span(h_dev, m, h_stride, w->rows, 2), span(g_dev, m, gu_stride, w->rows, 2),
+                           span(u_dev, m, gu_stride, w->rows, 2), piece(ws_dev, sp.bytes)};
     if (any_overlap(in, 3, out, 4) || pairs_overlap(out, 4)) return AFX_E_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(ws_dev);
@@ -285,12 +282,12 @@ int afx_restore_gated_backward_async(const afx_gated *w, uint32_t m, const float
         misaligned(dg_dev, 2) || misaligned(du_dev, 2) || misaligned(ws_dev, 16))
         return AFX_E_MISALIGNED;
     if (ws_bytes < sp.bytes) return AFX_E_BUFFER_TOO_SMALL;
-    const Span gu[] = {span(g_dev, m, gu_stride, w->rows, 2), span(u_dev, m, gu_stride, w->rows, 2)};
-    const Span in[] = {{w->gate_blob_dev, w->gate_info->blob_bytes},
-                       {w->up_blob_dev, w->up_info->blob_bytes},
-                       span(dh_dev, m, dh_stride, w->rows, 4)};
-    const Span out[] = {span(dx_dev, m, dx_stride, w->cols, 2), span(dg_dev, m, gu_stride, w->rows, 2),
-                        span(du_dev, m, gu_stride, w->rows, 2), {ws_dev, sp.bytes}};
+    const RowSpan gu[] = {span(g_dev, m, gu_stride, w->rows, 2), span(u_dev, m, gu_stride, w->rows, 2)};
+    const RowSpan in[] = {piece(w->gate_blob_dev, w->gate_info->blob_bytes),
+                          piece(w->up_blob_dev, w->up_info->blob_bytes),
+                          span(dh_dev, m, dh_stride, w->rows, 4)};
+    const RowSpan out[] = {span(dx_dev, m, dx_stride, w->cols, 2), span(dg_dev, m, gu_stride, w->rows, 2),
+                           span(du_dev, m, gu_stride, w->rows, 2), piece(ws_dev, sp.bytes)};
     if (any_overlap(in, 3, out, 4) || pairs_overlap(out, 4)) return AFX_E_INVALID_ARG;
     // g and u may be replaced in place by dg and du, and only so
     if (any_overlap(gu, 2, out, 1) || any_overlap(gu, 2, out + 3, 1)) return AFX_E_INVALID_ARG;
@@ -372,8 +369,8 @@ int afx_restore_gemm_t_async(const afx_info *info, const void *blob_dev, uint64_
     if (!d_dev || !y_dev || !ws_dev) return AFX_E_INVALID_ARG;
     if (misaligned(d_dev, 16) || misaligned(y_dev, 4) || misaligned(ws_dev, 16)) return AFX_E_MISALIGNED;
     if (ws_bytes < need) return AFX_E_BUFFER_TOO_SMALL;
-    const Span in[] = {{blob_dev, info->blob_bytes}, span(d_dev, m, rows, rows, 2)};
-    const Span out[] = {span(y_dev, m, cols, cols, 4), {ws_dev, need}};
+    const RowSpan in[] = {piece(blob_dev, info->blob_bytes), span(d_dev, m, rows, rows, 2)};
+    const RowSpan out[] = {span(y_dev, m, cols, cols, 4), piece(ws_dev, need)};
     if (any_overlap(in, 2, out, 2) || pairs_overlap(out, 2)) return AFX_E_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (transposed_fused(cols, m))

@@ -57,6 +57,26 @@ inline bool ranges_overlap(const void *a, uint64_t an, const void *b, uint64_t b
     return an && bn && a0 < b0 + bn && b0 < a0 + an;
 }
 
+// A buffer of rows `stride` bytes apart, `width` <= stride bytes each.
+struct RowSpan {
+    const void *p;
+    uint64_t rows, width, stride;
+    uint64_t bytes() const { return p && rows ? (rows - 1) * stride + width : 0; }
+};
+// Whether two buffers share a byte. Rows of one stride repeat with it, so
+// their places within it tell (column ranges of one wider matrix share none);
+// a single row is taken to have the other's stride. Of two strides, the
+// extents are compared, from the first byte to the last.
+inline bool rows_overlap(const RowSpan &a, const RowSpan &b) {
+    if (!ranges_overlap(a.p, a.bytes(), b.p, b.bytes())) return false;
+    const uint64_t stride = a.rows > 1 ? a.stride : b.stride;
+    if ((b.rows > 1 && b.stride != stride) || a.width > stride || b.width > stride || (a.rows == 1 && b.rows == 1))
+        return true;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    const uint64_t apart = b0 >= a0 ? (b0 - a0) % stride : (stride - (a0 - b0) % stride) % stride;
+    return apart < a.width || apart + b.width > stride;
+}
+
 // A batch of fused products writes each job's y while it reads every job's
 // blob and x: no y may share a byte with any of them (two jobs may add into
 // the same y, and share x).

@@ -464,8 +464,8 @@ int check_norm(const afx_block_norm *p) {
 
 constexpr uint64_t kMaxNormStride = 1ull << 28;  // (2^32 rows of them stay below 2^64 bytes)
 
-uint64_t rows_bytes(const Rows &r, uint32_t m, uint64_t d) {
-    return r.p && m ? ((uint64_t)(m - 1) * r.stride + d) * r.elem : 0;
+RowSpan span(const Rows &r, uint32_t m, uint64_t d) {  // (stride 0: one row for all)
+    return RowSpan{r.p, r.stride || m == 0 ? m : 1, d * r.elem, r.stride * r.elem};
 }
 
 // Strides, alignment, overlap (in_place: the pair of indices that may be one
@@ -482,8 +482,7 @@ int check_rows(const Rows *r, size_t n, uint32_t m, uint64_t d, size_t in0, size
     }
     for (size_t i = 0; i < n; ++i)
         for (size_t k = 0; k < n; ++k) {
-            if (i == k || !r[i].out || !ranges_overlap(r[i].p, rows_bytes(r[i], m, d), r[k].p, rows_bytes(r[k], m, d)))
-                continue;
+            if (i == k || !r[i].out || !rows_overlap(span(r[i], m, d), span(r[k], m, d))) continue;
             const bool pair = (i == in0 && k == in1) || (i == in1 && k == in0);
             if (!pair || r[i].p != r[k].p || r[i].stride != r[k].stride) return AFX_E_INVALID_ARG;
         }
@@ -595,11 +594,11 @@ int afx_block_norm_backward_async(const afx_block_norm *p, uint32_t m, const flo
                         {need ? ws_dev : nullptr, 0, 1, true}};
     for (int i = 0; i < 4; ++i) {
         if (reinterpret_cast<uintptr_t>(one[i].p) & (i < 3 ? 3 : 15)) return AFX_E_MISALIGNED;
-        const uint64_t n = i < 3 ? p->d * 4 : need;
+        const RowSpan mine{one[i].p, 1, i < 3 ? p->d * 4 : need, 0};
         for (const Rows &r : rows)
-            if (one[i].p && ranges_overlap(one[i].p, n, r.p, rows_bytes(r, m, p->d))) return AFX_E_INVALID_ARG;
+            if (rows_overlap(mine, span(r, m, p->d))) return AFX_E_INVALID_ARG;
         for (int k = 0; k < i; ++k)
-            if (one[i].p && one[k].p && ranges_overlap(one[i].p, n, one[k].p, p->d * 4)) return AFX_E_INVALID_ARG;
+            if (rows_overlap(mine, RowSpan{one[k].p, 1, p->d * 4, 0})) return AFX_E_INVALID_ARG;
     }
     if (ws_bytes < need) return AFX_E_BUFFER_TOO_SMALL;
     hipStream_t s = static_cast<hipStream_t>(stream);
