@@ -45,7 +45,11 @@ __device__ inline uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t
 
 // Elementwise, four values per thread; bound by memory (4 + 2 + 2 bytes read,
 // 4 or 8 written per value). The values go to the matrix cores as BF16: dg
-// and du are rounded once here, before dx is summed in FP32.
+// and du are rounded once here, before dx is summed in FP32. That costs dx as
+// much as its own rounding does (1.7e-3 of its norm each, 2.4e-3 together;
+// measured at 37 and 1024 tokens), and a second BF16 term for what the
+// rounding leaves would double the matrix instructions; so dx is the gradient
+// from the dg and du that the caller gets.
 template <uint32_t kAct>
 __global__ __launch_bounds__(256) void afx_gated_grad_kernel(const GradArgs p) {
     const uint32_t f = 4 * (blockIdx.x * 256 + threadIdx.x);
@@ -141,11 +145,14 @@ int check_sizes(uint64_t rows, uint64_t cols, uint32_t m) {
 }
 
 // Which kernels run a forward call. One to four tokens: the matrix-vector
-// kernel (two 17408 x 5120 matrices: 1 token 72 us, 4 102, where the next one
-// takes 100). Up to 128: the fused matrix-core kernel, if rows hold whole
-// groups of the coded format (128 tokens: 193 us, restored first 262; its sums
-// and operands have no room for more). Else the matrices are restored to the
-// workspace and multiplied there.
+// kernel. It and the next one, 3 tokens: two 17408 x 5120 matrices 81 and 89
+// us, 300 x 17408 19 and 43; 4 tokens: 88 and 89, 20 and 43, 8192 x 4096 42 and
+// 41, the worst for it 17408 x 512, 28 and 25; where the next one cannot run
+// (17408 x 5112, 4 tokens), 88 and, restored first, 223. Up to 128: the fused
+// matrix-core kernel, if rows hold whole groups of the coded format (it and
+// restored first, two 17408 x 5120 matrices: 16 tokens 92 and 214, 128 177 and
+// 229; 4096 x 2048, 128: 33 and 39; its sums and operands have no room for
+// more). Else the matrices are restored to the workspace and multiplied there.
 enum GatedPath { kPathGemv, kPathGemm, kPathRestore };
 GatedPath gated_path(uint64_t cols, uint32_t m) {
     if (m <= kGatedGemvTokens) return kPathGemv;
@@ -154,11 +161,12 @@ GatedPath gated_path(uint64_t cols, uint32_t m) {
 
 // Whether a transposed product takes the coded matrices as they are, or has
 // them restored to the workspace first. Fused and restored, rows of whole
-// groups: the gradient of two 17408 x 5120 matrices, 16 tokens 107 and 211
-// us, 64 138 and 215; 5120 x 17408, 64 tokens: 78 and 110. (Above 64 the fused
-// kernel's sums would not fit its registers.) Other rows decode a third more:
-// 5120 x 17400, 16 tokens: 76 and 111; but 37 tokens and two 4100 x 1528
-// matrices 37 and 34, 64 and 17408 x 5112 202 and 206.
+// groups: the gradient of two 17408 x 5120 matrices, 16 tokens 103 and 191
+// us, 64 125 and 200; 5120 x 17408, 64 tokens: 75 and 108; 1024 x 1024, 64: 18
+// and 22. (Above 64 the fused kernel's sums would not fit its registers.) Other
+// rows decode a third more: 5120 x 17400, 16 tokens: 75 and 104, two 4100 x
+// 1528 26 and 32; but 37 tokens and two 4100 x 1528 matrices 37 and 34, 64 and
+// 17408 x 5112 202 and 206.
 bool transposed_fused(uint64_t cols, uint32_t m) {
     return m <= (cols % kGroup == 0 ? kGemmTTokens : kGemmTTokensSplit);
 }

@@ -12,10 +12,14 @@
 // piece (x's own rows, 2 cols bytes apart, would fall into a few sets of the
 // L1).
 //
-// The decode's instructions and the coded bytes bound this, so the waves are
-// independent of each other: every wave stages its own rows' code words,
-// reads the workgroup's pair table, and shares no barrier after that is
-// built. They do go through the same columns at about the same time, so that
+// What bounds it: at 16 tokens (two 17408 x 5120 matrices, 89 us; their coded
+// bytes alone 40) vector instructions are issued for 47 us and LDS is busy for
+// 42, 61% of that in bank conflicts of the table's reads. Neither is full: a
+// wave's chains wait for one and the other in turn, and four waves a SIMD
+// hide only part of it. From there on the tokens' operands add to it (48
+// tokens: 118). So the waves are independent of each other: every wave stages
+// its own rows' code words, reads the workgroup's pair table, and shares no
+// barrier after that is built. They do go through the same columns at about the same time, so that
 // the CU's L1 serves most of their tokens' operands. The slabs of all tiles
 // (16 rows per wave), in order, are cut into one contiguous range per
 // workgroup; a range's sums for a tile go to the workspace in FP32, and a

@@ -11,11 +11,17 @@
 // load per 16 tokens; the sums of 128 columns stay in registers (32 per 16
 // tokens).
 //
-// The decode's instructions bound this (780 a slab, 31 us of the 55 that 16
-// tokens and a 5120 x 17408 matrix take). The slabs of a column tile, then of
-// the next, are cut into one contiguous range per workgroup, whose waves take
-// them in turn; the waves' sums are added through LDS, a tile's ranges by a
-// last launch, in order: the same bits on every run.
+// The decode bounds this: of the 56 us that 16 tokens and a 5120 x 17408 matrix
+// take (its coded bytes alone 20) vector instructions are issued for 28 (780 a
+// slab), LDS is busy for 24, half of it in bank conflicts of the table's reads,
+// and a wave waits for one of them, or for memory, in half of its time. 1.5
+// times the coded bytes are read (a slab needs only a part of the lines that
+// hold a row's gaps and code words; its neighbours come to them at other times).
+//
+// The slabs of a column tile, then of the next, are cut into one contiguous
+// range per workgroup, whose waves take them in turn; the waves' sums are
+// added through LDS, a tile's ranges by a last launch, in order: the same bits
+// on every run.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -19,7 +19,7 @@
 // (d <= 512) or a workgroup of up to 16 waves takes a row; each lane holds 8
 // values, 16 for d > 8192, 32 for d > 16384. (The gradients keep nine values
 // for each; 32 of them do not fit the registers: 1024 x 16384, BF16, 342 us
-// with 32, 128 with 16.)
+// with 32, 124 with 16; 1024 x 32768, where they must, 622.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -368,8 +368,9 @@ __global__ __launch_bounds__(kThreads) void afx_norm_grad_kernel(const NormArgs 
     }
 }
 
-// out[q] = sum over the workgroups' partial sums, in their order. 16 slices
-// of workgroups per column, then those in order.
+// out[q] = sum over the workgroups' partial sums. 32 slices per column: slice y
+// adds those of workgroups y, y + 32, .. in that order, and the slices are
+// added in theirs.
 constexpr uint32_t kSumSlices = 32, kSumCols = 32;
 __global__ __launch_bounds__(kSumSlices *kSumCols) void afx_norm_sum_kernel(const float *part, uint32_t groups,
                                                                             uint32_t d, float *o0, float *o1,
@@ -412,7 +413,7 @@ uint32_t norm_blocks(const NormShape &s, uint32_t m, uint32_t most) {
 }
 constexpr uint32_t kForwardBlocks = 8192;
 // Workgroups of the gradients' launch, each with its sums over its rows: one
-// on a CU from 10 waves on, more where they are small (4096 rows of 1024, 2
+// on a CU from 9 waves on, more where they are small (4096 rows of 1024, 2
 // waves each: 37 us with 1024 workgroups, 44 with 512; of 500 values, 4 waves:
 // 20 and 18).
 uint32_t grad_blocks(const NormShape &s, uint32_t m) {
