@@ -3,7 +3,8 @@
 // seg_staged): on streams of random code lengths, for every segment of small
 // and odd matrices, the lanes' groups start where the stream has them, and the
 // words staged reach to the segment's end, also where it is the tensor's last
-// one and crosses into the last chunk. The tiles, segments and clamps are
+// one and crosses into the last chunk; and on corrupt streams their count stays
+// within the slice. The tiles, segments and clamps are
 // composed here as the kernels compose them. Built with AddressSanitizer and
 // UndefinedBehaviorSanitizer by tests/test_segments.py; prints "segments ok"
 // and exits 0, else exits 1.
@@ -120,6 +121,12 @@ int main() {
     for (uint64_t rows = 1; rows <= 48; ++rows)
         for (uint64_t cols = 8; cols <= 360; cols += 8) all(rows, cols);
     for (int i = 0; i < 60; ++i) all(1 + rng() % 100, 8 * (1 + rng() % 700));
+    // whatever bases and gaps a corrupt stream holds, no more words than the slice has
+    for (int i = 0; i < 100000; ++i) {
+        const uint32_t end = seg_end((uint32_t)rng(), (uint32_t)rng(), (uint32_t)rng(), (uint32_t)rng() & 0xFFFF, (uint32_t)rng());
+        const uint64_t wa = seg_first_word(rng() >> rng() % 64);
+        CHECK(seg_staged(end, wa, kSegWords) <= kSegWords, "%u words staged", seg_staged(end, wa, kSegWords));
+    }
     if (g_fail) return 1;
     std::puts("segments ok");
     return 0;

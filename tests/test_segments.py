@@ -37,6 +37,8 @@ def test_segments(tmp_path):
      "return next & kSegLast ? stream_bits :", "return next & kSegLast ? base1 :"),
     ("the last segment's end taken for a group's", "const bool last = end >= left;", "const bool last = end > left;"),
     ("the end's chunk not told from the start's", "((in_chunk + end) / kChunk - ch) << 2", "0u"),
+    ("word count unclamped", "return umin32(((end - ((uint32_t)wa << 5) + 31) >> 5) + 1, most);",
+     "return ((end - ((uint32_t)wa << 5) + 31) >> 5) + 1;"),
     ("no word of look-ahead", "+ 31) >> 5) + 1, most);", "+ 31) >> 5), most);"),
 ])
 def test_check_catches_a_planted_mistake(tmp_path, what, old, new):
