@@ -396,6 +396,231 @@ int afx_block_norm_backward_async(const afx_block_norm *p, uint32_t m, const flo
                                   uint64_t dr_stride, uint16_t *db_dev, uint64_t db_stride, float *dw_pre_dev,
                                   float *dw_post_dev, float *dgate_dev, void *ws_dev, size_t ws_bytes, void *stream);
 
+/* ---- The attention half of a layer around the products: what stands between
+ * the q, k and v products and the attention, the attention of new tokens
+ * over a paged cache, and the cache's pages. Conventions (buffers, strides,
+ * workspaces) are those of the feed-forward half above. Page ids, lengths,
+ * slots and row starts are device memory that the host never reads: a value
+ * outside its range is treated as its call says and never reaches memory out
+ * of bounds. */
+
+#define AFX_MAX_HEAD_DIM 256u
+
+/* Keys and values of one layer, in pages of page_tokens tokens each:
+ *   k_dev: BF16 [n_pages][kv_heads][head_dim / 8][page_tokens][8]
+ *   v_dev: BF16 [n_pages][kv_heads][page_tokens / 8][head_dim][8]
+ * (the order in which the matrix cores take them: 8 consecutive dimensions of
+ * a key, 8 consecutive tokens of a value). A slot, page * page_tokens + its
+ * place in the page, names a token's place. */
+typedef struct afx_kv_pages {
+    uint16_t *k_dev, *v_dev; /* 16-byte aligned */
+    uint32_t n_pages;        /* n_pages * page_tokens < 2^31 */
+    uint32_t page_tokens;    /* 16, 32, 64, 128 or 256 */
+    uint32_t kv_heads;       /* 1..1024 */
+    uint32_t head_dim;       /* a multiple of 8 up to AFX_MAX_HEAD_DIM */
+} afx_kv_pages;
+
+/* Which two values of a head turn together. */
+typedef enum afx_pairing {
+    AFX_ROPE_HALVES = 0,    /* i and i + rot_dim / 2 */
+    AFX_ROPE_NEIGHBOURS = 1 /* 2 i and 2 i + 1 */
+} afx_pairing;
+
+/* Norm and rotary positions of the query and key heads:
+ *   n = x * rsqrt(mean(x^2) + eps) * w   over a head's values (w NULL: n = x)
+ *   a' = n_a cos t - n_b sin t, b' = n_b cos t + n_a sin t for every pair
+ *   (a, b) of the first rot_dim values, t = position[axis[i]] * freq[i] of
+ *   its pair i; the other values stay n.
+ * Positions may have several axes (time, height and width of images and
+ * video), each pair turning with one of them. */
+typedef struct afx_heads {
+    uint32_t q_heads, kv_heads; /* 1..1024 */
+    uint32_t head_dim;          /* a multiple of 8 up to AFX_MAX_HEAD_DIM */
+    uint32_t rot_dim;           /* even, 0..head_dim */
+    uint32_t pairing;           /* an afx_pairing */
+    uint32_t n_axes;            /* 1..4 */
+    float eps;                  /* > 0 (not used without w_q and w_k) */
+    const uint16_t *w_q, *w_k;  /* device, BF16 [head_dim], or NULL */
+    const float *freq;          /* device, FP32 [rot_dim / 2]: radians per position */
+    const uint8_t *axis;        /* device [rot_dim / 2], each below n_axes (larger: the last); NULL: all 0 */
+} afx_heads;
+
+/* afx_heads_async: norm and positions of m tokens' query and key heads, and
+ * the write of keys and values to the cache. q, k and v are FP32 rows (the
+ * products' y) of q_heads or kv_heads heads; pos is int32 [n_axes] rows of m,
+ * pos_stride apart (not read when rot_dim is 0; negative positions turn
+ * back). q NULL: no query heads; k NULL: no keys; v NULL: no values. q_out
+ * and k_out are BF16 rows; k_out may be NULL when kv is given. With kv, token
+ * i's key and value go to slot slots[i]; a slot outside the cache (such as
+ * -1) writes none. Slots inside it have to be distinct. Sums and rotations
+ * are FP32, angles FP64, and each output is rounded once. Any m (0 does
+ * nothing). Enqueued on stream; returns without waiting. Fastest when rot_dim
+ * and the strides are multiples of 8 and the buffers 16-byte aligned. Errors:
+ * AFX_E_INVALID_ARG (NULL pointer, nothing to do, a count out of its range,
+ * kv of other heads, v or slots without kv, q without q_out or the other way
+ * round, a stride shorter than its row, outputs sharing bytes with each other
+ * or an input), AFX_E_UNSUPPORTED (head_dim, page_tokens or the cache's size
+ * as above, a stride of 2^28 or more, m above 2^23), AFX_E_MISALIGNED,
+ * AFX_E_HIP. */
+int afx_heads_async(const afx_heads *p, uint32_t m, const int32_t *pos_dev, uint64_t pos_stride, const float *q_dev,
+                    uint64_t q_stride, const float *k_dev, uint64_t k_stride, const float *v_dev, uint64_t v_stride,
+                    uint16_t *q_out_dev, uint64_t q_out_stride, uint16_t *k_out_dev, uint64_t k_out_stride,
+                    const afx_kv_pages *kv, const int32_t *slots_dev, void *stream);
+
+/* afx_heads_workspace: bytes of device workspace that
+ * afx_heads_backward_async needs for m tokens. Host only. */
+int afx_heads_workspace(const afx_heads *p, uint32_t m, size_t *bytes);
+
+/* afx_heads_backward_async: the gradients of afx_heads_async from its inputs
+ * q and k and the gradients dq and dk (BF16) of q_out and k_out: dq_in and
+ * dk_in BF16 (afx_restore_gemm_t_async's d), dw_q and dw_k FP32 [head_dim],
+ * summed over tokens and heads in an order that depends on the sizes only
+ * (the same bits on every run; zeros with m == 0). dq NULL: nothing of the
+ * query heads, dk NULL: nothing of the keys. dq_in may be dq itself with the
+ * same stride, dk_in dk. q (k) is only read where w_q (w_k) is given and may
+ * else be NULL. dq_in, dk_in, dw_q and dw_k may each be NULL (not computed).
+ * Errors: as afx_heads_async; AFX_E_INVALID_ARG for dw_q without w_q or dq
+ * (dw_k likewise) where m is not 0, AFX_E_BUFFER_TOO_SMALL (workspace, only
+ * needed for dw_q and dw_k). */
+int afx_heads_backward_async(const afx_heads *p, uint32_t m, const int32_t *pos_dev, uint64_t pos_stride,
+                             const float *q_dev, uint64_t q_stride, const float *k_dev, uint64_t k_stride,
+                             const uint16_t *dq_dev, uint64_t dq_stride, const uint16_t *dk_dev, uint64_t dk_stride,
+                             uint16_t *dq_in_dev, uint64_t dq_in_stride, uint16_t *dk_in_dev, uint64_t dk_in_stride,
+                             float *dw_q_dev, float *dw_k_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* Which pages hold the tokens of n_seqs sequences: token j of sequence s is at
+ * place j % page_tokens of page table[s][j / page_tokens]. Entries behind a
+ * sequence's last page are -1. refs counts how many sequences hold a page; 0
+ * is a free one. All three are changed by the afx_pages calls only. */
+typedef struct afx_page_table {
+    int32_t *table_dev;    /* [n_seqs] rows of max_pages, table_stride apart */
+    uint64_t table_stride; /* elements */
+    int32_t *len_dev;      /* [n_seqs]: tokens */
+    int32_t *refs_dev;     /* [n_pages] (afx_attend_async does not read it: may be NULL there) */
+    uint32_t n_seqs, max_pages, n_pages, page_tokens;
+} afx_page_table;
+
+/* Attention of new tokens. */
+typedef struct afx_attend {
+    uint32_t q_heads;  /* a multiple of the cache's kv_heads; q_heads / kv_heads <= 256 */
+    float scale;       /* finite */
+    uint32_t causal;   /* 0: every token sees its sequence's whole cache */
+    uint32_t window;   /* 0: none; else a token sees itself and the window - 1 tokens before it (and, not causal,
+                          those after it) */
+    uint32_t max_new;  /* the most new tokens of a sequence and the most tokens of one, by which the */
+    uint32_t max_len;  /* work is divided: larger ones come out right too, but take longer */
+} afx_attend;
+
+/* afx_attend_workspace: bytes of device workspace that afx_attend_async needs
+ * for n_rows sequences with m new tokens in all. Host only. */
+int afx_attend_workspace(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t m, size_t *bytes);
+
+/* afx_attend_async: out = softmax(scale q k^T) v for the new tokens of n_rows
+ * sequences over the cache, which already holds them. Row r's new tokens are
+ * rows starts[r] .. starts[r + 1] - 1 of q and out (starts: device, n_rows + 1
+ * values from 0 to m, not decreasing; a row may have none), and belong to
+ * sequence seqs[r] (seqs NULL: r). With len tokens in the sequence and n new
+ * ones, new token i stands at position len - n + i and sees the positions up
+ * to its own (causal), within its window. Query head h reads key and value
+ * head h / (q_heads / kv_heads). q and out are BF16 rows of q_heads heads;
+ * lse, if not NULL, is FP32 [m][q_heads]: the natural logarithm of the sum of
+ * e^score. A query that sees nothing (or only scores of minus infinity) gets
+ * zeros and an lse of minus infinity. Rows of q behind the last start are not
+ * read, and those of out and lse are left as they were. What a query does not
+ * see never changes its result, infinities and NaN in it included. Tokens of
+ * a page whose id is outside the cache are seen by none, rows whose sequence
+ * is outside the table have no tokens, lengths are capped at max_pages pages,
+ * and starts at m. Scores and sums are FP32; the weights of the values are
+ * rounded to BF16 (the matrix cores' operand), as is out. The same bits on
+ * every run. Enqueued on stream; returns without waiting. Errors:
+ * AFX_E_INVALID_ARG (NULL pointer, a count out of its range, a table of other
+ * pages, a stride shorter than its row, outputs sharing bytes with each other
+ * or an input), AFX_E_UNSUPPORTED (the cache's sizes as above, m above 2^23,
+ * n_rows above 2^16, a stride of 2^28 or more), AFX_E_MISALIGNED (q, out not
+ * 16-byte aligned or strides not multiples of 8), AFX_E_BUFFER_TOO_SMALL. */
+int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page_table *t, uint32_t n_rows,
+                     const int32_t *seqs_dev, const int32_t *starts_dev, uint32_t m, const uint16_t *q_dev,
+                     uint64_t q_stride, uint16_t *out_dev, uint64_t out_stride, float *lse_dev, void *ws_dev,
+                     size_t ws_bytes, void *stream);
+
+/* ---- The cache's pages. These calls change tables, lengths and counts on the
+ * GPU, without waiting and without the host seeing them, so that steps of
+ * generation may be captured in a HIP graph. Each gives one result, whatever
+ * runs at the same time inside it: that of taking its rows in their order.
+ * Calls that share a table have to follow one another on a stream. Lists hold
+ * at most AFX_MAX_PAGE_ROWS rows (AFX_E_UNSUPPORTED). Errors of all:
+ * AFX_E_INVALID_ARG (NULL pointer, a zero size, table_stride below max_pages,
+ * buffers sharing bytes), AFX_E_UNSUPPORTED (page_tokens not a power of two
+ * from 16 to 256, n_pages * page_tokens or max_pages * page_tokens of 2^31 or
+ * more, n_seqs above 2^20, table_stride of 2^28 or more), AFX_E_MISALIGNED,
+ * AFX_E_BUFFER_TOO_SMALL (workspace), AFX_E_HIP. */
+
+#define AFX_MAX_PAGE_ROWS 1024u
+
+/* What the pages hold: n_planes arrays of n_pages pages (keys and values of
+ * every layer), each page page_bytes long (a multiple of 16). */
+typedef struct afx_page_data {
+    void *data_dev;        /* 16-byte aligned */
+    uint64_t page_bytes;   /* a multiple of 16, up to 2^30 */
+    uint64_t plane_stride; /* bytes between planes: a multiple of 16, at least n_pages * page_bytes */
+    uint32_t n_planes;     /* 1..65535 */
+} afx_page_data;
+
+/* afx_pages_fork_async: sequence dst[r] becomes a copy of src[r] that shares
+ * all of its pages (their counts rise by one); no page is copied until one of
+ * the holders grows into it. A row is refused, and changes nothing, if either
+ * id is outside the table, dst[r] holds tokens, dst[r] is the dst of an
+ * earlier row, or src[r] is the dst of any row. granted (int32 [n], may be
+ * NULL) tells 1 or 0 for each row. */
+int afx_pages_fork_async(const afx_page_table *t, uint32_t n, const int32_t *src_dev, const int32_t *dst_dev,
+                         int32_t *granted_dev, void *stream);
+
+/* afx_pages_trim_async: sequence seqs[r] keeps its first lens[r] tokens (lens
+ * NULL: none: it is freed); pages behind them are given up (their counts fall
+ * by one). A length of 0 or less frees, one above the sequence's changes
+ * nothing. Rows with ids outside the table, or named in an earlier row, are
+ * passed over. */
+int afx_pages_trim_async(const afx_page_table *t, uint32_t n, const int32_t *seqs_dev, const int32_t *lens_dev,
+                         void *stream);
+
+/* afx_pages_extend_workspace: bytes of device workspace that
+ * afx_pages_extend_async needs for n rows. Host only. */
+int afx_pages_extend_workspace(const afx_page_table *t, uint32_t n, size_t *bytes);
+
+/* afx_pages_extend_async: sequence seqs[r] grows by the starts[r + 1] -
+ * starts[r] tokens of row r (as in afx_attend_async, m in all). It gets the
+ * pages that it needs, the free ones of the lowest ids, rows in their order;
+ * if its last page is partly filled and held by others too, it first gets a
+ * copy of its own (of rows that share such a page, the last holder keeps it).
+ * A row for which too few pages are left is refused with all rows after it; a
+ * row is also refused if its id is outside the table or named in an earlier
+ * row, or if the sequence would exceed max_pages pages. granted[r] (may be
+ * NULL) is the number of tokens by which it grew. slots[i] is the slot of
+ * token i (-1 for tokens of refused rows and those behind the last start),
+ * pos[i] (may be NULL) its position in the sequence (0 there). The new slots'
+ * contents are what they were. */
+int afx_pages_extend_async(const afx_page_table *t, const afx_page_data *d, uint32_t n, const int32_t *seqs_dev,
+                           const int32_t *starts_dev, uint32_t m, int32_t *slots_dev, int32_t *pos_dev,
+                           int32_t *granted_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* afx_pages_compact_workspace: bytes of device workspace of
+ * afx_pages_compact_async. Host only. */
+int afx_pages_compact_workspace(const afx_page_table *t, size_t *bytes);
+
+/* afx_pages_compact_async: the live pages (count above 0) move to the lowest
+ * ids: with `live` of them, the k-th one at an id of `live` or more moves to
+ * the k-th free id below it, the others stay. Tables and counts follow. map
+ * (int32 [n_pages]) is each page's new id, -1 for free ones; live (int32 [1],
+ * may be NULL) the number of live pages: what stays behind them is free. */
+int afx_pages_compact_async(const afx_page_table *t, const afx_page_data *d, int32_t *map_dev, int32_t *live_dev,
+                            void *ws_dev, size_t ws_bytes, void *stream);
+
+/* afx_pages_copy_async: in every plane, page dst[i] becomes a copy of page
+ * src[i], for n pairs (any n; 0 does nothing). Pairs with an id outside the
+ * n_pages pages are passed over. No dst may be named twice or be a src. */
+int afx_pages_copy_async(const afx_page_data *d, uint32_t n_pages, uint32_t n, const int32_t *src_dev,
+                         const int32_t *dst_dev, void *stream);
+
 /* ---- Unpack on the host. "Why Weight Offloading Slows Inference" (section
  * "The path from storage to the GPU", Figure 1) unpacks a compressed weight
  * in RAM between the read and the copy to the GPU, and section "Lossless

@@ -29,6 +29,9 @@ AFX_READ_DIRECT = 1
 ACT_SILU, ACT_GELU_TANH, ACT_GELU = 0, 1, 2
 TYPE_BF16, TYPE_FP32 = 0, 1
 MAX_NORM_WIDTH = 32768
+ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1
+MAX_HEAD_DIM = 256
+MAX_PAGE_ROWS = 1024
 
 # Every symbol include/afx.h declares.
 EXPORTS = ("afx_query", "afx_decode_tensor", "afx_decode_layer_async", "afx_decode_layer_grid_async",
@@ -38,7 +41,11 @@ EXPORTS = ("afx_query", "afx_decode_tensor", "afx_decode_layer_async", "afx_deco
            "afx_restore_gemm_batch_async",
            "afx_restore_gated_workspace", "afx_restore_gated_async", "afx_restore_gated_backward_async",
            "afx_restore_gemm_t_workspace", "afx_restore_gemm_t_async",
-           "afx_block_norm_async", "afx_block_norm_workspace", "afx_block_norm_backward_async")
+           "afx_block_norm_async", "afx_block_norm_workspace", "afx_block_norm_backward_async",
+           "afx_heads_async", "afx_heads_workspace", "afx_heads_backward_async",
+           "afx_attend_workspace", "afx_attend_async",
+           "afx_pages_fork_async", "afx_pages_trim_async", "afx_pages_extend_workspace", "afx_pages_extend_async",
+           "afx_pages_compact_workspace", "afx_pages_compact_async", "afx_pages_copy_async")
 
 
 class AfxError(RuntimeError):
@@ -118,6 +125,66 @@ class afx_block_norm(ctypes.Structure):
     ]
 
 
+class afx_kv_pages(ctypes.Structure):
+    _fields_ = [
+        ("k_dev", ctypes.c_void_p),
+        ("v_dev", ctypes.c_void_p),
+        ("n_pages", ctypes.c_uint32),
+        ("page_tokens", ctypes.c_uint32),
+        ("kv_heads", ctypes.c_uint32),
+        ("head_dim", ctypes.c_uint32),
+    ]
+
+
+class afx_heads(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_uint32),
+        ("kv_heads", ctypes.c_uint32),
+        ("head_dim", ctypes.c_uint32),
+        ("rot_dim", ctypes.c_uint32),
+        ("pairing", ctypes.c_uint32),
+        ("n_axes", ctypes.c_uint32),
+        ("eps", ctypes.c_float),
+        ("w_q", ctypes.c_void_p),
+        ("w_k", ctypes.c_void_p),
+        ("freq", ctypes.c_void_p),
+        ("axis", ctypes.c_void_p),
+    ]
+
+
+class afx_page_table(ctypes.Structure):
+    _fields_ = [
+        ("table_dev", ctypes.c_void_p),
+        ("table_stride", ctypes.c_uint64),
+        ("len_dev", ctypes.c_void_p),
+        ("refs_dev", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_uint32),
+        ("max_pages", ctypes.c_uint32),
+        ("n_pages", ctypes.c_uint32),
+        ("page_tokens", ctypes.c_uint32),
+    ]
+
+
+class afx_attend(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_uint32),
+        ("scale", ctypes.c_float),
+        ("causal", ctypes.c_uint32),
+        ("window", ctypes.c_uint32),
+        ("max_new", ctypes.c_uint32),
+        ("max_len", ctypes.c_uint32),
+    ]
+
+
+class afx_page_data(ctypes.Structure):
+    _fields_ = [
+        ("data_dev", ctypes.c_void_p),
+        ("page_bytes", ctypes.c_uint64),
+        ("plane_stride", ctypes.c_uint64),
+        ("n_planes", ctypes.c_uint32),
+    ]
+
+
 _lib = None
 
 
@@ -166,6 +233,9 @@ def lib() -> ctypes.CDLL:
         L.afx_restore_gemm_batch_async.restype = ctypes.c_int
         ptr, u32, u64, size = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t
         sizep, gatedp, normp = ctypes.POINTER(size), ctypes.POINTER(afx_gated), ctypes.POINTER(afx_block_norm)
+        headsp, kvp, tablep = (ctypes.POINTER(afx_heads), ctypes.POINTER(afx_kv_pages),
+                               ctypes.POINTER(afx_page_table))
+        attendp, datap = ctypes.POINTER(afx_attend), ctypes.POINTER(afx_page_data)
         for name, args in (
                 ("afx_restore_gated_workspace", [u64, u64, u32, ctypes.c_int, sizep]),
                 ("afx_restore_gated_async", [gatedp, u32, ptr, u64, ptr, u64, ptr, ptr, u64, ptr, size, ptr]),
@@ -178,7 +248,23 @@ def lib() -> ctypes.CDLL:
                 ("afx_block_norm_workspace", [normp, u32, sizep]),
                 ("afx_block_norm_backward_async",
                  [normp, u32, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, ptr, ptr, ptr, size,
-                  ptr])):
+                  ptr]),
+                ("afx_heads_async",
+                 [headsp, u32, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, kvp, ptr, ptr]),
+                ("afx_heads_workspace", [headsp, u32, sizep]),
+                ("afx_heads_backward_async",
+                 [headsp, u32, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, u64, ptr, ptr, ptr, size,
+                  ptr]),
+                ("afx_attend_workspace", [attendp, kvp, u32, u32, sizep]),
+                ("afx_attend_async",
+                 [attendp, kvp, tablep, u32, ptr, ptr, u32, ptr, u64, ptr, u64, ptr, ptr, size, ptr]),
+                ("afx_pages_fork_async", [tablep, u32, ptr, ptr, ptr, ptr]),
+                ("afx_pages_trim_async", [tablep, u32, ptr, ptr, ptr]),
+                ("afx_pages_extend_workspace", [tablep, u32, sizep]),
+                ("afx_pages_extend_async", [tablep, datap, u32, ptr, ptr, u32, ptr, ptr, ptr, ptr, size, ptr]),
+                ("afx_pages_compact_workspace", [tablep, sizep]),
+                ("afx_pages_compact_async", [tablep, datap, ptr, ptr, ptr, size, ptr]),
+                ("afx_pages_copy_async", [datap, u32, u32, ptr, ptr, ptr])):
             getattr(L, name).argtypes = args
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -438,6 +524,141 @@ def afx_block_norm_backward_async(p: afx_block_norm, m: int, b_dev: int, b_strid
                                                dxn_dev, dxn_stride, dr_out_dev, dr_out_stride, dr_dev, dr_stride,
                                                db_dev, db_stride, dw_pre_dev, dw_post_dev, dgate_dev, ws_dev, ws_bytes,
                                                stream), "afx_block_norm_backward_async")
+
+
+def kv_pages(k_dev: int, v_dev: int, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> afx_kv_pages:
+    """One layer's pages of keys and values (see afx.h for their order)."""
+    return afx_kv_pages(k_dev, v_dev, _u32(n_pages, "n_pages"), _u32(page_tokens, "page_tokens"),
+                        _u32(kv_heads, "kv_heads"), _u32(head_dim, "head_dim"))
+
+
+def heads(q_heads: int, kv_heads: int, head_dim: int, rot_dim: int, pairing: int = ROPE_HALVES, n_axes: int = 1,
+          eps: float = 1e-6, w_q: int = 0, w_k: int = 0, freq: int = 0, axis: int = 0) -> afx_heads:
+    """Norm and rotary positions of query and key heads: device addresses of
+    the norms' weights, the frequencies and each pair's axis, 0 for those it
+    does without."""
+    return afx_heads(_u32(q_heads, "q_heads"), _u32(kv_heads, "kv_heads"), _u32(head_dim, "head_dim"),
+                     _u32(rot_dim, "rot_dim"), _u32(pairing, "pairing"), _u32(n_axes, "n_axes"), eps, w_q, w_k, freq,
+                     axis)
+
+
+def afx_heads_async(p: afx_heads, m: int, pos_dev: int, pos_stride: int, q_dev: int, q_stride: int, k_dev: int,
+                    k_stride: int, v_dev: int, v_stride: int, q_out_dev: int, q_out_stride: int, k_out_dev: int,
+                    k_out_stride: int, kv: afx_kv_pages | None, slots_dev: int, stream: int = 0) -> None:
+    """Norm and positions of m tokens' heads, keys and values to their slots of
+    the cache; an address of 0 (or kv None) leaves that part out (see afx.h)."""
+    _check(lib().afx_heads_async(ctypes.byref(p), _u32(m, "m"), pos_dev, pos_stride, q_dev, q_stride, k_dev, k_stride,
+                                 v_dev, v_stride, q_out_dev, q_out_stride, k_out_dev, k_out_stride,
+                                 ctypes.byref(kv) if kv is not None else None, slots_dev, stream), "afx_heads_async")
+
+
+def afx_heads_workspace(p: afx_heads, m: int) -> int:
+    """Bytes of device workspace of afx_heads_backward_async."""
+    n = ctypes.c_size_t()
+    _check(lib().afx_heads_workspace(ctypes.byref(p), _u32(m, "m"), ctypes.byref(n)), "afx_heads_workspace")
+    return n.value
+
+
+def afx_heads_backward_async(p: afx_heads, m: int, pos_dev: int, pos_stride: int, q_dev: int, q_stride: int,
+                             k_dev: int, k_stride: int, dq_dev: int, dq_stride: int, dk_dev: int, dk_stride: int,
+                             dq_in_dev: int, dq_in_stride: int, dk_in_dev: int, dk_in_stride: int, dw_q_dev: int,
+                             dw_k_dev: int, ws_dev: int, ws_bytes: int, stream: int = 0) -> None:
+    """The gradients of afx_heads_async; an address of 0 leaves an output
+    uncomputed (see afx.h)."""
+    _check(lib().afx_heads_backward_async(ctypes.byref(p), _u32(m, "m"), pos_dev, pos_stride, q_dev, q_stride, k_dev,
+                                          k_stride, dq_dev, dq_stride, dk_dev, dk_stride, dq_in_dev, dq_in_stride,
+                                          dk_in_dev, dk_in_stride, dw_q_dev, dw_k_dev, ws_dev, ws_bytes, stream),
+           "afx_heads_backward_async")
+
+
+def page_table(table_dev: int, table_stride: int, len_dev: int, refs_dev: int, n_seqs: int, max_pages: int,
+               n_pages: int, page_tokens: int) -> afx_page_table:
+    """Which pages hold the tokens of n_seqs sequences (device int32 arrays)."""
+    return afx_page_table(table_dev, table_stride, len_dev, refs_dev, _u32(n_seqs, "n_seqs"),
+                          _u32(max_pages, "max_pages"), _u32(n_pages, "n_pages"), _u32(page_tokens, "page_tokens"))
+
+
+def page_data(data_dev: int, page_bytes: int, plane_stride: int, n_planes: int) -> afx_page_data:
+    """What the pages hold: n_planes arrays of pages, plane_stride bytes apart."""
+    return afx_page_data(data_dev, page_bytes, plane_stride, _u32(n_planes, "n_planes"))
+
+
+def attend(q_heads: int, scale: float, causal: bool = True, window: int = 0, max_new: int = 1,
+           max_len: int = 0) -> afx_attend:
+    """Attention of new tokens: max_new and max_len are the most new tokens,
+    and tokens, of a sequence, by which the work is divided."""
+    return afx_attend(_u32(q_heads, "q_heads"), scale, int(causal), _u32(window, "window"), _u32(max_new, "max_new"),
+                      _u32(max_len, "max_len"))
+
+
+def afx_attend_workspace(p: afx_attend, kv: afx_kv_pages, n_rows: int, m: int) -> int:
+    """Bytes of device workspace of afx_attend_async."""
+    n = ctypes.c_size_t()
+    _check(lib().afx_attend_workspace(ctypes.byref(p), ctypes.byref(kv), _u32(n_rows, "n_rows"), _u32(m, "m"),
+                                      ctypes.byref(n)), "afx_attend_workspace")
+    return n.value
+
+
+def afx_attend_async(p: afx_attend, kv: afx_kv_pages, t: afx_page_table, n_rows: int, seqs_dev: int, starts_dev: int,
+                     m: int, q_dev: int, q_stride: int, out_dev: int, out_stride: int, lse_dev: int, ws_dev: int,
+                     ws_bytes: int, stream: int = 0) -> None:
+    """out = softmax(scale q k^T) v of the new tokens of n_rows sequences over
+    the paged cache; seqs_dev 0: row r is sequence r; lse_dev may be 0 (see
+    afx.h)."""
+    _check(lib().afx_attend_async(ctypes.byref(p), ctypes.byref(kv), ctypes.byref(t), _u32(n_rows, "n_rows"), seqs_dev,
+                                  starts_dev, _u32(m, "m"), q_dev, q_stride, out_dev, out_stride, lse_dev, ws_dev,
+                                  ws_bytes, stream), "afx_attend_async")
+
+
+def afx_pages_fork_async(t: afx_page_table, n: int, src_dev: int, dst_dev: int, granted_dev: int,
+                         stream: int = 0) -> None:
+    """Sequences dst become copies of src that share their pages (see afx.h)."""
+    _check(lib().afx_pages_fork_async(ctypes.byref(t), _u32(n, "n"), src_dev, dst_dev, granted_dev, stream),
+           "afx_pages_fork_async")
+
+
+def afx_pages_trim_async(t: afx_page_table, n: int, seqs_dev: int, lens_dev: int, stream: int = 0) -> None:
+    """Sequences keep their first lens tokens; lens_dev 0 frees them (see afx.h)."""
+    _check(lib().afx_pages_trim_async(ctypes.byref(t), _u32(n, "n"), seqs_dev, lens_dev, stream),
+           "afx_pages_trim_async")
+
+
+def afx_pages_extend_workspace(t: afx_page_table, n: int) -> int:
+    """Bytes of device workspace of afx_pages_extend_async."""
+    b = ctypes.c_size_t()
+    _check(lib().afx_pages_extend_workspace(ctypes.byref(t), _u32(n, "n"), ctypes.byref(b)),
+           "afx_pages_extend_workspace")
+    return b.value
+
+
+def afx_pages_extend_async(t: afx_page_table, d: afx_page_data, n: int, seqs_dev: int, starts_dev: int, m: int,
+                           slots_dev: int, pos_dev: int, granted_dev: int, ws_dev: int, ws_bytes: int,
+                           stream: int = 0) -> None:
+    """Sequences grow by the new tokens of their rows, which get slots (see
+    afx.h); pos_dev and granted_dev may be 0."""
+    _check(lib().afx_pages_extend_async(ctypes.byref(t), ctypes.byref(d), _u32(n, "n"), seqs_dev, starts_dev,
+                                        _u32(m, "m"), slots_dev, pos_dev, granted_dev, ws_dev, ws_bytes, stream),
+           "afx_pages_extend_async")
+
+
+def afx_pages_compact_workspace(t: afx_page_table) -> int:
+    """Bytes of device workspace of afx_pages_compact_async."""
+    b = ctypes.c_size_t()
+    _check(lib().afx_pages_compact_workspace(ctypes.byref(t), ctypes.byref(b)), "afx_pages_compact_workspace")
+    return b.value
+
+
+def afx_pages_compact_async(t: afx_page_table, d: afx_page_data, map_dev: int, live_dev: int, ws_dev: int,
+                            ws_bytes: int, stream: int = 0) -> None:
+    """The live pages move to the lowest ids; live_dev may be 0 (see afx.h)."""
+    _check(lib().afx_pages_compact_async(ctypes.byref(t), ctypes.byref(d), map_dev, live_dev, ws_dev, ws_bytes,
+                                         stream), "afx_pages_compact_async")
+
+
+def afx_pages_copy_async(d: afx_page_data, n_pages: int, n: int, src_dev: int, dst_dev: int, stream: int = 0) -> None:
+    """In every plane, pages dst become copies of pages src (see afx.h)."""
+    _check(lib().afx_pages_copy_async(ctypes.byref(d), _u32(n_pages, "n_pages"), _u32(n, "n"), src_dev, dst_dev,
+                                      stream), "afx_pages_copy_async")
 
 
 def afx_decode_host(blob, blob_bytes: int | None = None, out=None, threads: int = 0):
