@@ -19,7 +19,8 @@ SOURCES = [os.path.join(CSRC, "afx_host.cpp"), os.path.join(CSRC, "afx_io.cpp"),
            os.path.join(CSRC, "afx_gated_gemm.hip"), os.path.join(CSRC, "afx_gemm_t.hip"),
            os.path.join(CSRC, "afx_mm.hip"), os.path.join(CSRC, "afx_panels.hip"),
            os.path.join(CSRC, "afx_norm.hip"), os.path.join(CSRC, "afx_heads.hip"),
-           os.path.join(CSRC, "afx_attend.hip"), os.path.join(CSRC, "afx_pages.hip")]
+           os.path.join(CSRC, "afx_attend.hip"), os.path.join(CSRC, "afx_attend_few.hip"),
+           os.path.join(CSRC, "afx_attend_many.hip"), os.path.join(CSRC, "afx_pages.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-FP32 instructions are kept out of every device build.

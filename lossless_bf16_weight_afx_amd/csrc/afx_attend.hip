@@ -1,110 +1,162 @@
-// afx_attend.hip -- attention of new tokens over a paged cache (gfx950).
+// afx_attend.hip -- attention of new tokens over a paged cache (gfx950): entry
+// points, the division of the work, and the join of parts.
 //
 //   o = sum_j e^(s_j - M) v_j / sum_j e^(s_j - M),  s_j = scale q k_j,
 //   lse = M + ln sum_j e^(s_j - M)
 // over the positions j that the query sees; M is the running maximum of one
-// pass over them.
-#include <hip/hip_runtime.h>
-
+// pass over them. Batch rows of a few query rows a head go to
+// afx_attend_few.hip, which memory bounds, the others to
+// afx_attend_many.hip, which the matrix cores bound. Where there are too few
+// workgroups to fill the card, tokens are cut into parts, whose sums (FP32) a
+// last launch joins: with M the largest of the parts' M_i,
+//   o = sum_i 2^(M_i - M) o_i / sum_i 2^(M_i - M) l_i.
 #include <algorithm>
 #include <cmath>
 
-#include "afx_paged.h"
+#include "afx_attend.h"
 
 namespace afx {
 namespace {
 
 constexpr uint32_t kMaxRows = 1u << 16, kMaxGroup = 256;
+constexpr uint32_t kJoinThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 
-struct AttendArgs {
-    const uint16_t *q, *k, *v;
-    uint16_t *out;
-    float *lse;
-    const int32_t *table, *len, *seqs, *starts;
-    uint64_t q_stride, out_stride, table_stride;
-    uint32_t m, n_rows, n_seqs, max_pages, n_pages, page_shift, q_heads, kv_heads, group, d, causal, window;
-    float scale;
-};
-
-__device__ inline float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// A batch row's sequence, its new tokens and its length.
-struct Row {
-    uint32_t seq, from, n, len;  // n == 0: nothing to do
-    __device__ Row(const AttendArgs &a, uint32_t r) {
-        seq = a.seqs ? (uint32_t)a.seqs[r] : r;
-        from = (uint32_t)min(max(a.starts[r], 0), (int32_t)a.m);
-        const uint32_t to = (uint32_t)min(max(a.starts[r + 1], 0), (int32_t)a.m);
-        n = to > from ? to - from : 0;
-        len = seq < a.n_seqs ? (uint32_t)min((int64_t)max(a.len[seq], 0), (int64_t)a.max_pages << a.page_shift) : 0;
+// The parts of one query row of a batch row that the kernel for few rows took,
+// by a workgroup: teams of d / 4 lanes add up every n-th part, then the teams.
+__global__ __launch_bounds__(kJoinThreads) void afx_attend_join_few_kernel(AttendArgs a) {
+    __shared__ float weight[kMaxSplits];
+    __shared__ f32x4 sums[kJoinThreads];
+    __shared__ float tops[kJoinThreads / 64], totals[kJoinThreads / 64];
+    const uint32_t rr = blockIdx.x % a.few_rows, kvh = blockIdx.x / a.few_rows % a.kv_heads;
+    const uint32_t r = blockIdx.x / a.few_rows / a.kv_heads;
+    const BatchRow row(a, r);
+    if (rr >= row.n * a.group || row.n * a.group > a.few_rows) return;
+    const uint32_t n = FewRange(a, row).splits;
+    if (n == 1) return;
+    const uint64_t p = (uint64_t)blockIdx.x * a.few_splits;
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const float2 ml = threadIdx.x < n ? a.few_ml[p + threadIdx.x] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+    weight[threadIdx.x] = f;
+    float sum = f * ml.y;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) sum += __shfl_xor(sum, o);
+    if (lane == 0) totals[wave] = sum;
+    __syncthreads();
+    sum = (totals[0] + totals[1]) + (totals[2] + totals[3]);
+    const uint32_t quads = a.d / 4, teams = kJoinThreads / quads, team = threadIdx.x / quads, quad = threadIdx.x % quads;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    if (team < teams) {
+#pragma unroll 4
+        for (uint32_t i = team; i < n; i += teams) {
+            const float w = weight[i];
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(a.few_o + (p + i) * a.d + 4 * quad);
+            if (w != 0.f) o += w * v;
+        }
     }
-};
+    sums[threadIdx.x] = o;
+    __syncthreads();
+    if (team) return;
+    for (uint32_t i = 1; i < teams; ++i) o += sums[i * quads + quad];
+    const float k = sum == 0.f ? 0.f : 1.f / sum;
+    if (sum == 0.f) o = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint64_t t = row.from + rr / a.group;
+    const uint32_t h = kvh * a.group + rr % a.group;
+    *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * a.d + 4 * quad) =
+        make_uint2(pack2(o[0] * k, o[1] * k), pack2(o[2] * k, o[3] * k));
+    if (a.lse && quad == 0) a.lse[t * a.q_heads + h] = lse_of(top, sum);
+}
 
-__global__ __launch_bounds__(64) void afx_attend_kernel(AttendArgs a) {
-    __shared__ float q[AFX_MAX_HEAD_DIM], p[64];
-    __shared__ int32_t ids[64];
-    const uint32_t t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x, size = 1u << a.page_shift;
-    uint32_t lo = 0, hi = a.n_rows;  // the last row that starts at t or before
+// The parts of query rows that the kernel for many rows took, a team of
+// lanes (4 values each) per token and head.
+__global__ __launch_bounds__(kJoinThreads) void afx_attend_join_many_kernel(AttendArgs a) {
+    const uint32_t quads = a.d / 4, teams = kJoinThreads / quads;
+    const uint32_t team = threadIdx.x / quads, quad = threadIdx.x % quads;
+    const uint64_t at = (uint64_t)blockIdx.x * teams + team;
+    if (team >= teams || at >= (uint64_t)a.m * a.q_heads) return;
+    const uint32_t t = (uint32_t)(at / a.q_heads), h = (uint32_t)(at % a.q_heads);
+    uint32_t lo = 0, hi = a.n_rows;  // the last batch row that starts at t or before
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) / 2;
         if (a.starts[mid] <= (int32_t)t) lo = mid; else hi = mid;
     }
-    const Row row(a, lo);
-    if (t < row.from || t >= row.from + row.n) return;
-    const int64_t at = (int64_t)row.len - row.n + (t - row.from);
-    const int64_t end = a.causal ? min(at + 1, (int64_t)row.len) : (int64_t)row.len;
-    const int64_t begin = a.window ? max(at - (int64_t)a.window + 1, (int64_t)0) : 0;
-    for (uint32_t i = lane; i < a.d; i += 64) q[i] = from_bf16(a.q[t * a.q_stride + h * a.d + i]) * a.scale;
-    __syncthreads();
-    const uint64_t head = (uint64_t)(h / a.group) * size * a.d, page_elems = (uint64_t)size * a.kv_heads * a.d;
-    const int32_t *table = a.table + row.seq * a.table_stride;
-    float top = -INFINITY, sum = 0.f, o[4] = {};
-    for (int64_t j0 = begin; j0 < end; j0 += 64) {
-        const uint32_t j = (uint32_t)j0 + lane;
-        const uint32_t id = j < end ? (uint32_t)table[j / size] : ~0u;
-        const bool seen = id < a.n_pages;
-        float s = -INFINITY;
-        if (seen) {
-            s = 0.f;
-            const uint16_t *k = a.k + id * page_elems + head + j % size * 8;
-            for (uint32_t c = 0; c < a.d; ++c) s += q[c] * from_bf16(k[c / 8 * size * 8 + c % 8]);
-        }
-        float best = s;
-        for (int x = 1; x < 64; x *= 2) best = fmaxf(best, __shfl_xor(best, x));
-        const float now = fmaxf(top, best), base = now == -INFINITY ? 0.f : now;
-        const float old = __expf(top - base);
-        __syncthreads();
-        p[lane] = seen ? __expf(s - base) : 0.f;
-        ids[lane] = seen ? (int32_t)id : -1;
-        float part = p[lane];
-        for (int x = 1; x < 64; x *= 2) part += __shfl_xor(part, x);
-        sum = sum * old + part;
-        top = now;
-        __syncthreads();
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t c = lane + 64 * e;
-            if (c >= a.d) break;
-            o[e] *= old;
-            for (uint32_t i = 0; i < 64; ++i) {
-                if (ids[i] < 0) continue;
-                const uint32_t off = ((uint32_t)j0 + i) % size;
-                o[e] += p[i] * from_bf16(a.v[(uint32_t)ids[i] * page_elems + head + ((off & ~7u) * a.d) + c * 8 + off % 8]);
-            }
-        }
+    const BatchRow row(a, lo);
+    if (t < row.from || t >= row.from + row.n || row.n * a.group <= a.few_rows) return;
+    const uint64_t p = at * a.many_splits;
+    float top = -INFINITY, sum = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t i = 0; i < a.many_splits; ++i) top = fmaxf(top, a.many_ml[p + i].x);
+#pragma unroll 4
+    for (uint32_t i = 0; i < a.many_splits; ++i) {
+        const float2 ml = a.many_ml[p + i];
+        const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(a.many_o + (p + i) * a.d + 4 * quad);
+        sum += w * ml.y;
+        if (w != 0.f) o += w * v;
     }
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t c = lane + 64 * e;
-        if (c < a.d)
-            a.out[t * a.out_stride + h * a.d + c] = __builtin_bit_cast(uint16_t, (__bf16)(sum == 0.f ? 0.f : o[e] / sum));
+    const float k = sum == 0.f ? 0.f : 1.f / sum;
+    if (sum == 0.f) o = f32x4{0.f, 0.f, 0.f, 0.f};
+    *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * a.d + 4 * quad) =
+        make_uint2(pack2(o[0] * k, o[1] * k), pack2(o[2] * k, o[3] * k));
+    if (a.lse && quad == 0) a.lse[at] = lse_of(top, sum);
+}
+
+// ---- the division of the work --------------------------------------------------
+uint64_t up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+    uint32_t few_rows, few_part, few_splits, many_tiles, many_splits;
+    uint64_t few_sums, many_sums;  // rows of sums of parts
+    uint64_t bytes(uint32_t d) const { return (few_sums + many_sums) * 4ull * (d + 2); }
+};
+
+// Depends on the parameters and sizes only, as the order of the sums does.
+Plan plan(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t m) {
+    Plan s{};
+    const uint32_t group = p->q_heads / kv->kv_heads;
+    const uint64_t most = std::max<uint64_t>(1, std::min(p->max_new, m));  // new tokens of a sequence
+    uint64_t tokens = std::max<uint64_t>(1, p->max_len);                   // that its queries see
+    if (p->window) tokens = std::min<uint64_t>(tokens, (p->causal ? 0 : tokens) + p->window + most);
+    const bool few = most * group <= 32, many = !few;
+    s.few_rows = few ? (uint32_t)(most * group) : n_rows > 1 ? 32 : 0;
+    s.few_part = 1u << 30;
+    s.few_splits = 1;
+    s.many_splits = 1;
+    if (s.few_rows) {
+        // about 2048 workgroups, of 256 tokens at least
+        const uint64_t all = tokens * kv->kv_heads * n_rows;
+        s.few_part = (uint32_t)std::max<uint64_t>(256, up(up(all, 2048), 128) * 128);
+        s.few_part = (uint32_t)std::max<uint64_t>(s.few_part, up(up(tokens, kMaxSplits), 128) * 128);
+        s.few_splits = (uint32_t)up(tokens, s.few_part);
+        if (s.few_splits > 1) s.few_sums = (uint64_t)n_rows * kv->kv_heads * s.few_rows * s.few_splits;
     }
-    if (a.lse && lane == 0) a.lse[(uint64_t)t * a.q_heads + h] = sum == 0.f ? -INFINITY : top + __logf(sum);
+    if (many) {
+        const uint64_t tiles = up((uint64_t)m * group, kManyRows);
+        s.many_tiles = (uint32_t)((uint64_t)m * group / kManyRows + n_rows);
+        // whole rounds of two workgroups a CU, parts of 256 tokens at least
+        const uint64_t most_splits = std::min<uint64_t>(16, std::max<uint64_t>(1, tokens / 256));
+        double best = 1e30;
+        for (uint64_t n = 1; n <= most_splits; ++n) {
+            const double cost = (double)up(tiles * kv->kv_heads * n, 512) / (double)n * (1 + 0.02 * (double)(n - 1));
+            if (cost < best * 0.98) best = cost, s.many_splits = (uint32_t)n;
+        }
+        if (s.many_splits > 1) s.many_sums = (uint64_t)m * p->q_heads * s.many_splits;
+    }
+    return s;
 }
 
 int check_attend(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t m) {
     const int rc = check_kv(kv);
     if (rc != AFX_OK) return rc;
     if (!p || p->q_heads == 0 || p->q_heads % kv->kv_heads || p->q_heads / kv->kv_heads > kMaxGroup ||
-        !std::isfinite(p->scale))
+        !std::isfinite(p->scale * kLog2e))
         return AFX_E_INVALID_ARG;
     return n_rows > kMaxRows || m > kMaxTokens ? AFX_E_UNSUPPORTED : AFX_OK;
 }
@@ -120,7 +172,7 @@ int afx_attend_workspace(const afx_attend *p, const afx_kv_pages *kv, uint32_t n
     const int rc = check_attend(p, kv, n_rows, m);
     if (rc != AFX_OK) return rc;
     if (!bytes) return AFX_E_INVALID_ARG;
-    *bytes = 0;
+    *bytes = plan(p, kv, n_rows, m).bytes(kv->head_dim);
     return AFX_OK;
 }
 
@@ -139,8 +191,16 @@ int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page
     if (q_stride >= kMaxRowStride || out_stride >= kMaxRowStride) return AFX_E_UNSUPPORTED;
     if (q_stride % 8 || out_stride % 8 || !aligned({q_dev, out_dev}, 16) || !aligned({seqs_dev, starts_dev, lse_dev}, 4))
         return AFX_E_MISALIGNED;
+    const Plan w = plan(p, kv, n_rows, m);
+    const uint64_t need = w.bytes(kv->head_dim);
+    if ((uint64_t)kv->kv_heads * std::max((uint64_t)n_rows * std::max(w.few_rows, 1u),
+                                          (uint64_t)w.many_tiles * w.many_splits) >= 1ull << 24)
+        return AFX_E_UNSUPPORTED;
+    if (need && !ws_dev) return AFX_E_INVALID_ARG;
+    if (need && !aligned({ws_dev}, 16)) return AFX_E_MISALIGNED;
     const RowSpan s[] = {RowSpan{out_dev, m, 2 * width, 2 * out_stride},
                          flat(lse_dev, 4ull * m * p->q_heads),
+                         flat(ws_dev, need),
                          RowSpan{q_dev, m, 2 * width, 2 * q_stride},
                          flat(kv->k_dev, kv_bytes(kv)),
                          flat(kv->v_dev, kv_bytes(kv)),
@@ -148,7 +208,8 @@ int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page
                          flat(t->len_dev, 4ull * t->n_seqs),
                          flat(seqs_dev, 4ull * n_rows),
                          flat(starts_dev, 4ull * n_rows + 4)};
-    if (outputs_overlap(s, 2, 9)) return AFX_E_INVALID_ARG;
+    if (outputs_overlap(s, 3, 10)) return AFX_E_INVALID_ARG;
+    if (ws_bytes < need) return AFX_E_BUFFER_TOO_SMALL;
     AttendArgs a{};
     a.q = q_dev;
     a.k = kv->k_dev;
@@ -174,12 +235,32 @@ int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page
     a.d = kv->head_dim;
     a.causal = p->causal;
     a.window = p->window;
-    a.scale = p->scale;
+    a.scale2 = p->scale == 0.f ? 1.f : std::fabs(p->scale) * kLog2e;
+    a.q_and = p->scale == 0.f ? 0 : ~0u;
+    a.q_xor = p->scale < 0.f ? 0x80008000u : 0;
+    a.few_rows = w.few_rows;
+    a.few_part = w.few_part;
+    a.few_splits = w.few_splits;
+    a.many_tiles = w.many_tiles;
+    a.many_splits = w.many_splits;
+    a.few_o = static_cast<float *>(ws_dev);
+    a.many_o = a.few_o + w.few_sums * a.d;
+    a.few_ml = reinterpret_cast<float2 *>(a.many_o + w.many_sums * a.d);
+    a.many_ml = a.few_ml + w.few_sums;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (w.many_tiles) rc = launch_attend_many(a, st);
+    if (rc == AFX_OK && w.few_rows) rc = launch_attend_few(a, st);
     void *args[] = {&a};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&afx_attend_kernel), dim3(m, p->q_heads), dim3(64), args, 0,
-                           static_cast<hipStream_t>(stream)) == hipSuccess
-               ? AFX_OK
-               : AFX_E_HIP;
+    auto join = [&](const void *fn, uint64_t blocks) {
+        return hipLaunchKernel(fn, dim3((uint32_t)blocks), dim3(kJoinThreads), args, 0, st) == hipSuccess ? AFX_OK
+                                                                                                       : AFX_E_HIP;
+    };
+    if (rc == AFX_OK && w.few_sums)
+        rc = join(reinterpret_cast<const void *>(&afx_attend_join_few_kernel), (uint64_t)n_rows * a.kv_heads * a.few_rows);
+    if (rc == AFX_OK && w.many_sums)
+        rc = join(reinterpret_cast<const void *>(&afx_attend_join_many_kernel),
+                  up((uint64_t)m * a.q_heads, kJoinThreads / (a.d / 4)));
+    return rc;
 }
 
 }  // extern "C"

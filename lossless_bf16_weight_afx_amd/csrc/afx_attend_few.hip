@@ -1,0 +1,349 @@
+// afx_attend_few.hip -- attention of few query rows (one or a few new tokens
+// a sequence) over a paged cache: generation (gfx950).
+//
+// Reading the cache once bounds it. A workgroup of 4 waves takes one
+// key-value head of a batch row, or one part of its tokens; each wave takes
+// every fourth tile of 32 tokens on its own, and the waves' sums meet in LDS
+// at the end. Keys and values go from memory to the matrix cores' operand
+// registers as they lie in the pages, 16 bytes a lane, no LDS in between:
+//   S^T = K Q^T    v_mfma_f32_16x16x32_bf16, K rows (tokens) as A, query rows
+//                  as B: a lane holds 4 tokens' scores of one query row;
+//   O^T += V^T P^T V^T rows (dimensions) as A, the weights as B.
+// Two score tiles of 16 tokens take their rows from tokens 8 (i / 4) + i mod 4
+// and 4 more, so that lane group g (lanes 16 g ..) ends up with the scores of
+// tokens 8 g .. 8 g + 7, which is what it has to feed as B: the weights never
+// leave their lane.
+//
+// The next tile's keys are requested when this tile's scores are done with
+// them, its values after the second product: one of both is always on its
+// way. The running maximum moves only when a score exceeds it by 8 (a factor
+// 2^8): most tiles exchange nothing between lanes. Weights then lie in 0..2^8
+// and lose nothing, as their rounding to BF16 is relative.
+#include <type_traits>
+
+#include "afx_attend.h"
+
+namespace afx {
+namespace {
+
+constexpr uint32_t kWaves = 4, kThreads = 64 * kWaves;
+constexpr float kSlack = 8.f;
+
+// One wave's state: for each of RG groups of 16 query rows, the lane's row is
+// lane mod 16 of it.
+template <int KC, int RG>
+struct Wave {
+    static constexpr int kDT = 2 * KC;  // tiles of 16 dimensions
+    bf16x8 q[RG][KC];
+    f32x4 o[RG][kDT];
+    float top[RG], sum[RG];
+    int32_t begin[RG], end[RG];  // positions that the lane's row sees
+};
+
+struct Where {
+    const int32_t *table;
+    const uint16_t *k, *v;  // of page 0's head
+    uint32_t page_elems, size, shift, d;
+    int32_t lo, hi;      // positions that all rows see
+    int32_t first, last; // and any
+};
+
+// 8 tokens' worth of a value fragment without the tokens that ok leaves out.
+__device__ inline u32x4 only(u32x4 v, uint32_t ok) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] &= ((ok >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((ok >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
+    return v;
+}
+
+// Whether one of 8 values is an infinity or NaN.
+__device__ inline bool odd(u32x4 v) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t |= (v[i] & 0x7F807F80u) + 0x00800080u;  // (only all ones carry into bit 15)
+    return t & 0x80008000u;
+}
+
+// One pass over the wave's tiles from j0 to j1. kFull: a head has 32 KC
+// dimensions, none of a fragment lies behind them.
+template <int KC, int RG, bool kFull>
+__device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC, RG> &s, int32_t j0, int32_t j1,
+                                    uint32_t wave, uint32_t lane) {
+    constexpr int kDT = 2 * KC;
+    const uint32_t c = lane & 15, g = lane >> 4;
+    const uint32_t chunks = w.d / 8;
+#pragma unroll
+    for (int x = 0; x < RG; ++x) {
+        s.top[x] = -INFINITY;
+        s.sum[x] = 0.f;
+#pragma unroll
+        for (int t = 0; t < kDT; ++t) s.o[x][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    int32_t j = j0 + (int32_t)(wave * kFewTokens);
+    if (j >= j1) return;
+    // page ids of the lane's key tokens (8 (c / 4) ..) and value tokens (8 g ..)
+    auto page_of = [&](int32_t at) {
+        return (uint32_t)w.table[min((uint32_t)at >> w.shift, a.max_pages - 1)];
+    };
+    u32x4 kf[2][KC], vf[kDT];
+    auto load_k = [&](int32_t at, uint32_t id) {
+        const uint32_t tok = (uint32_t)at + 8 * (c >> 2) + (c & 3);
+        const uint16_t *p = w.k + (uint64_t)(id < a.n_pages ? id : 0) * w.page_elems + (tok & (w.size - 1)) * 8;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+            const uint32_t chunk = 4 * kc + g;
+            const uint16_t *pc = p + (kFull ? chunk : min(chunk, chunks - 1)) * w.size * 8;
+            kf[0][kc] = *reinterpret_cast<const u32x4 *>(pc);
+            kf[1][kc] = *reinterpret_cast<const u32x4 *>(pc + 32);
+        }
+    };
+    auto load_v = [&](int32_t at, uint32_t id) {
+        const uint32_t tok = ((uint32_t)at + 8 * g) & (w.size - 1);
+        const uint16_t *p = w.v + (uint64_t)(id < a.n_pages ? id : 0) * w.page_elems + tok * w.d;
+#pragma unroll
+        for (int t = 0; t < kDT; ++t)
+            vf[t] = *reinterpret_cast<const u32x4 *>(p + (kFull ? 16 * t + c : min(16 * t + c, w.d - 1)) * 8);
+    };
+    constexpr int32_t kStep = kWaves * kFewTokens;
+    uint32_t kid = page_of(j + 8 * (c >> 2)), vid = page_of(j + 8 * g);
+    uint32_t kid2 = page_of(j + kStep + 8 * (c >> 2)), vid2 = page_of(j + kStep + 8 * g);
+    load_k(j, kid);
+    load_v(j, vid);
+    for (; j < j1; j += kStep) {
+        f32x4 sc[RG][2];
+#pragma unroll
+        for (int x = 0; x < RG; ++x) sc[x][0] = sc[x][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                u32x4 f = kf[y][kc];
+                if (!kFull && kc >= KC - 2 && 4 * kc + g >= chunks) f = u32x4{0, 0, 0, 0};  // behind the head's dimensions
+#pragma unroll
+                for (int x = 0; x < RG; ++x)
+                    sc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), s.q[x][kc],
+                                                                       sc[x][y], 0, 0, 0);
+            }
+        const uint32_t id = vid;
+        const bool more = j + kStep < j1;
+        const uint32_t kid3 = page_of(j + 2 * kStep + 8 * (c >> 2)), vid3 = page_of(j + 2 * kStep + 8 * g);
+        if (more) load_k(j + kStep, kid2);
+        const bool clean = j >= w.lo && j + (int32_t)kFewTokens <= w.hi && __all(id < a.n_pages);
+        uint32_t any = 0xFF;  // of the lane's 8 tokens, those that some row sees
+        if (!clean) {
+            any = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int32_t at = j + 8 * (int32_t)g + e;
+                any |= id < a.n_pages && at >= w.first && at < w.last ? 1u << e : 0u;
+            }
+        }
+        bf16x8 p[RG];
+#pragma unroll
+        for (int x = 0; x < RG; ++x) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = sc[x][e / 4][e % 4];
+            if (!clean) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int32_t at = j + 8 * (int32_t)g + e;
+                    if (id >= a.n_pages || at < s.begin[x] || at >= s.end[x]) v[e] = -INFINITY;
+                }
+            }
+            float best = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+            best *= a.scale2;
+            if (__any(best > s.top[x] + kSlack)) {
+                best = fmaxf(best, __shfl_xor(best, 16));
+                best = fmaxf(best, __shfl_xor(best, 32));
+                const float now = fmaxf(s.top[x], best);
+                const float f = now == -INFINITY ? 1.f : exp2_fast(s.top[x] - now);
+                s.top[x] = now;
+                s.sum[x] *= f;
+#pragma unroll
+                for (int t = 0; t < kDT; ++t) s.o[x][t] *= f;
+            }
+            const float base = s.top[x] == -INFINITY ? 0.f : s.top[x];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = exp2_fast(__builtin_fmaf(v[e], a.scale2, -base));
+            s.sum[x] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[x][e] = (__bf16)v[e];
+        }
+        bool strange = false;
+        if (!clean) {
+#pragma unroll
+            for (int t = 0; t < kDT; ++t) {
+                vf[t] = only(vf[t], any);
+                strange |= odd(vf[t]);
+            }
+        }
+        if (!clean && __any(strange)) {
+            // value by value, so that an infinity or NaN reaches only the rows that see it
+            const uint32_t dims = opaque(w.d), own = opaque(4 * g);
+#pragma unroll 1
+            for (int e = 0; e < (int)kFewTokens; ++e) {
+                const int32_t at = j + e;
+                const uint32_t page = __shfl(id, 16 * (e / 8));
+                if (page >= a.n_pages) continue;
+                const uint16_t *pv = w.v + (uint64_t)page * w.page_elems + (at & (w.size - 1) & ~7u) * dims + at % 8;
+#pragma unroll
+                for (int x = 0; x < RG; ++x) {
+                    const u32x4 bits = __builtin_bit_cast(u32x4, p[x]);
+                    const uint32_t two = e / 2 % 4 == 0 ? bits[0] : e / 2 % 4 == 1 ? bits[1] : e / 2 % 4 == 2 ? bits[2] : bits[3];
+                    const uint32_t got = __shfl(two, c + 16 * (e / 8));
+                    const float weight = from_bf16((uint16_t)(e % 2 ? got >> 16 : got));
+                    if (at >= s.begin[x] && at < s.end[x])
+#pragma unroll
+                        for (int t = 0; t < kDT; ++t)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const uint32_t dim = 16 * t + own + r;
+                                if (dim < dims) s.o[x][t][r] += weight * from_bf16(pv[dim * 8]);
+                            }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < kDT; ++t)
+#pragma unroll
+                for (int x = 0; x < RG; ++x)
+                    s.o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf[t]), p[x], s.o[x][t],
+                                                                        0, 0, 0);
+        }
+        if (more) load_v(j + kStep, vid2);
+        vid = vid2;
+        kid2 = kid3;
+        vid2 = vid3;
+    }
+}
+
+template <int KC>
+struct Lds {
+    float o[kWaves][16][32 * KC + 4];
+    float2 ml[kWaves][16];
+};
+
+// What a workgroup works on: a key-value head of batch row r, or one part of
+// its tokens, j0 .. j1 - 1.
+struct Part {
+    BatchRow row;
+    uint32_t r, kvh, part, splits;
+    int32_t j0, j1;
+};
+
+// The query rows from r0 on.
+template <int KC, int RG, bool kFull>
+__device__ __forceinline__ void unit(const AttendArgs &a, const Part &t, uint32_t r0, Lds<KC> &lds) {
+    constexpr int kDT = 2 * KC;
+    const BatchRow &row = t.row;
+    const int32_t j0 = t.j0, j1 = t.j1;
+    const uint32_t r = t.r, kvh = t.kvh, part = t.part;
+    const uint32_t tid = opaque(threadIdx.x), lane = tid % 64, wave = tid / 64, c = lane & 15, g = lane >> 4;
+    const uint32_t rows = row.n * a.group;
+    Where w;
+    w.table = a.table + (row.seq < a.n_seqs ? row.seq : 0) * a.table_stride;
+    w.size = 1u << a.page_shift;
+    w.shift = a.page_shift;
+    w.d = a.d;
+    w.page_elems = w.size * a.kv_heads * a.d;
+    w.k = a.k + (uint64_t)kvh * w.size * a.d;
+    w.v = a.v + (uint64_t)kvh * w.size * a.d;
+    const uint32_t last = min(r0 + 16 * RG, rows) - 1;
+    w.first = row.begin(a, r0 / a.group);
+    w.last = row.end(a, last / a.group);
+    w.lo = row.begin(a, last / a.group);
+    w.hi = row.end(a, r0 / a.group);
+    Wave<KC, RG> s;
+#pragma unroll
+    for (int x = 0; x < RG; ++x) {
+        const uint32_t rr = min(r0 + 16 * x + c, last), t = rr / a.group;
+        s.begin[x] = row.begin(a, t);
+        s.end[x] = row.end(a, t);
+        const uint16_t *q = a.q + (row.from + t) * a.q_stride + (kvh * a.group + rr % a.group) * a.d;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) s.q[x][kc] = load_q(a, q, 32 * kc + 8 * g);
+    }
+    run<KC, RG, kFull>(a, w, s, j0, j1, wave, lane);
+    // the waves' sums, 16 rows at a time
+#pragma unroll
+    for (int x = 0; x < RG; ++x) {
+        s.sum[x] += __shfl_xor(s.sum[x], 16);
+        s.sum[x] += __shfl_xor(s.sum[x], 32);
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < kDT; ++t) *reinterpret_cast<f32x4 *>(&lds.o[wave][c][16 * t + 4 * g]) = s.o[x][t];
+        if (g == 0) lds.ml[wave][c] = make_float2(s.top[x], s.sum[x]);
+        __syncthreads();
+        const uint32_t quads = a.d / 4;
+        for (uint32_t i = tid; i < 16 * quads; i += kThreads) {
+            const uint32_t at = i / quads, quad = i % quads, rr = r0 + 16 * x + at;
+            if (rr >= rows) break;
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (uint32_t v = 0; v < kWaves; ++v) top = fmaxf(top, lds.ml[v][at].x);
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (uint32_t v = 0; v < kWaves; ++v) {
+                const float2 ml = lds.ml[v][at];
+                const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+                sum += f * ml.y;
+                if (f != 0.f) o += f * *reinterpret_cast<const f32x4 *>(&lds.o[v][at][4 * quad]);
+            }
+            const uint32_t tok = row.from + rr / a.group, h = kvh * a.group + rr % a.group;
+            if (t.splits == 1) {
+                const float k = sum == 0.f ? 0.f : 1.f / sum;
+                if (sum == 0.f) o = f32x4{0.f, 0.f, 0.f, 0.f};
+                *reinterpret_cast<uint2 *>(a.out + tok * a.out_stride + h * a.d + 4 * quad) =
+                    make_uint2(pack2(o[0] * k, o[1] * k), pack2(o[2] * k, o[3] * k));
+                if (a.lse && quad == 0) a.lse[(uint64_t)tok * a.q_heads + h] = lse_of(top, sum);
+            } else {
+                const uint64_t p = (((uint64_t)r * a.kv_heads + kvh) * a.few_rows + rr) * a.few_splits + part;
+                *reinterpret_cast<f32x4 *>(a.few_o + p * a.d + 4 * quad) = o;
+                if (quad == 0) a.few_ml[p] = make_float2(top, sum);
+            }
+        }
+    }
+}
+
+template <int KC, int RG, bool kFull>
+__global__ __launch_bounds__(kThreads, KC * RG <= 8 ? 2 : 1) void afx_attend_few_kernel(AttendArgs a) {
+    __shared__ Lds<KC> lds;
+    Part t;
+    t.kvh = blockIdx.x % a.kv_heads, t.r = blockIdx.x / a.kv_heads, t.part = blockIdx.y;
+    t.row = BatchRow(a, t.r);
+    const uint32_t rows = t.row.n * a.group;
+    if (rows == 0 || (a.many_tiles && rows > a.few_rows)) return;
+    const FewRange range(a, t.row);
+    t.splits = range.splits;
+    if (t.part >= t.splits) return;
+    t.j0 = range.base + (int32_t)(t.part * a.few_part);
+    t.j1 = t.part + 1 == t.splits ? range.end : t.j0 + (int32_t)a.few_part;
+    for (uint32_t r0 = 0; r0 < rows; r0 += 16 * RG)
+        unit<KC, RG, kFull>(a, t, r0, lds);
+}
+
+}  // namespace
+
+int launch_attend_few(const AttendArgs &a, hipStream_t stream) {
+    AttendArgs args = a;
+    void *p[] = {&args};
+    auto go = [&](auto kc) {
+        constexpr int KC = decltype(kc)::value;
+        auto pick = [](auto *f) { return reinterpret_cast<const void *>(f); };
+        const bool one = a.few_rows <= 16;
+        const void *fn = a.d == 32 * KC ? one ? pick(&afx_attend_few_kernel<KC, 1, true>) : pick(&afx_attend_few_kernel<KC, 2, true>)
+                         : one          ? pick(&afx_attend_few_kernel<KC, 1, false>)
+                                        : pick(&afx_attend_few_kernel<KC, 2, false>);
+        return hipLaunchKernel(fn, dim3(a.kv_heads * a.n_rows, a.few_splits), dim3(kThreads), p, 0, stream) == hipSuccess
+                   ? AFX_OK
+                   : AFX_E_HIP;
+    };
+    if (a.d <= 64) return go(std::integral_constant<int, 2>{});
+    if (a.d <= 96) return go(std::integral_constant<int, 3>{});
+    if (a.d <= 128) return go(std::integral_constant<int, 4>{});
+    if (a.d <= 192) return go(std::integral_constant<int, 6>{});
+    return go(std::integral_constant<int, 8>{});
+}
+
+}  // namespace afx
