@@ -20,6 +20,7 @@ namespace {
 
 constexpr uint32_t kMaxRows = 1u << 16, kMaxGroup = 256;
 constexpr uint32_t kJoinThreads = 256;
+constexpr uint32_t kTeamParts = 16;  // parts that a team of d / 4 lanes joins by itself
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The parts of one query row of a batch row that the kernel for few rows took,
@@ -74,8 +75,57 @@ __global__ __launch_bounds__(kJoinThreads) void afx_attend_join_few_kernel(Atten
     if (a.lse && quad == 0) a.lse[t * a.q_heads + h] = lse_of(top, sum);
 }
 
-// The parts of query rows that the kernel for many rows took, a team of
-// lanes (4 values each) per token and head.
+// One query row's parts p .. p + n - 1, by a team of d / 4 lanes that hold 4
+// values each: one pass, 8 parts' loads at a time in flight.
+__device__ inline void join_row(const AttendArgs &a, const float *po, const float2 *pml, uint64_t p, uint32_t n,
+                                uint32_t quad, uint64_t t, uint32_t h) {
+    constexpr uint32_t kAtOnce = 8;
+    float top = -INFINITY, sum = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t i0 = 0; i0 < n; i0 += kAtOnce) {
+        float2 ml[kAtOnce];
+        f32x4 v[kAtOnce];
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) {
+            const uint64_t at = p + min(i0 + i, n - 1);
+            ml[i] = pml[at];
+            v[i] = *reinterpret_cast<const f32x4 *>(po + at * a.d + 4 * quad);
+        }
+        float now = top;
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) now = fmaxf(now, ml[i].x);
+        const float base = now == -INFINITY ? 0.f : now, old = exp2_fast(top - base);
+        top = now;
+        sum *= old;
+        o *= old;
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) {
+            const float w = i0 + i < n && ml[i].x != -INFINITY ? exp2_fast(ml[i].x - base) : 0.f;
+            sum += w * ml[i].y;
+            if (w != 0.f) o += w * v[i];
+        }
+    }
+    const float k = sum == 0.f ? 0.f : 1.f / sum;
+    if (sum == 0.f) o = f32x4{0.f, 0.f, 0.f, 0.f};
+    *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * a.d + 4 * quad) =
+        make_uint2(pack2(o[0] * k, o[1] * k), pack2(o[2] * k, o[3] * k));
+    if (a.lse && quad == 0) a.lse[t * a.q_heads + h] = lse_of(top, sum);
+}
+
+// Up to kTeamParts parts of the query rows that the kernel for few rows took, a team a row.
+__global__ __launch_bounds__(kJoinThreads) void afx_attend_join_teams_kernel(AttendArgs a) {
+    const uint32_t quads = a.d / 4, teams = kJoinThreads / quads;
+    const uint32_t team = threadIdx.x / quads, quad = threadIdx.x % quads;
+    const uint64_t at = (uint64_t)blockIdx.x * teams + team;
+    if (team >= teams || at >= (uint64_t)a.n_rows * a.kv_heads * a.few_rows) return;
+    const uint32_t rr = (uint32_t)(at % a.few_rows), kvh = (uint32_t)(at / a.few_rows % a.kv_heads);
+    const BatchRow row(a, (uint32_t)(at / a.few_rows / a.kv_heads));
+    if (rr >= row.n * a.group || row.n * a.group > a.few_rows) return;
+    const uint32_t n = FewRange(a, row).splits;
+    if (n > 1) join_row(a, a.few_o, a.few_ml, at * a.few_splits, n, quad, row.from + rr / a.group, kvh * a.group + rr % a.group);
+}
+
+// The parts of query rows that the kernel for many rows took, a team per token and head.
 __global__ __launch_bounds__(kJoinThreads) void afx_attend_join_many_kernel(AttendArgs a) {
     const uint32_t quads = a.d / 4, teams = kJoinThreads / quads;
     const uint32_t team = threadIdx.x / quads, quad = threadIdx.x % quads;
@@ -89,23 +139,7 @@ __global__ __launch_bounds__(kJoinThreads) void afx_attend_join_many_kernel(Atte
     }
     const BatchRow row(a, lo);
     if (t < row.from || t >= row.from + row.n || row.n * a.group <= a.few_rows) return;
-    const uint64_t p = at * a.many_splits;
-    float top = -INFINITY, sum = 0.f;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t i = 0; i < a.many_splits; ++i) top = fmaxf(top, a.many_ml[p + i].x);
-#pragma unroll 4
-    for (uint32_t i = 0; i < a.many_splits; ++i) {
-        const float2 ml = a.many_ml[p + i];
-        const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(a.many_o + (p + i) * a.d + 4 * quad);
-        sum += w * ml.y;
-        if (w != 0.f) o += w * v;
-    }
-    const float k = sum == 0.f ? 0.f : 1.f / sum;
-    if (sum == 0.f) o = f32x4{0.f, 0.f, 0.f, 0.f};
-    *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * a.d + 4 * quad) =
-        make_uint2(pack2(o[0] * k, o[1] * k), pack2(o[2] * k, o[3] * k));
-    if (a.lse && quad == 0) a.lse[at] = lse_of(top, sum);
+    join_row(a, a.many_o, a.many_ml, at * a.many_splits, a.many_splits, quad, t, h);
 }
 
 // ---- the division of the work --------------------------------------------------
@@ -130,11 +164,21 @@ Plan plan(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t
     s.few_splits = 1;
     s.many_splits = 1;
     if (s.few_rows) {
-        // about 2048 workgroups, of 256 tokens at least
-        const uint64_t all = tokens * kv->kv_heads * n_rows;
-        s.few_part = (uint32_t)std::max<uint64_t>(256, up(up(all, 2048), 128) * 128);
-        s.few_part = (uint32_t)std::max<uint64_t>(s.few_part, up(up(tokens, kMaxSplits), 128) * 128);
-        s.few_splits = (uint32_t)up(tokens, s.few_part);
+        // Parts of 256 tokens at least. A part's start and end cost about as much as 128 tokens, a join as 490, and
+        // two workgroups of a CU share its reads: the cheapest number for rows of equal lengths and rows of any
+        // (0.55 of the longest, the last part alone) together. Times by tokens of a part, 40 query and 8 key-value
+        // heads of 128:
+        //   64 rows of 8192 tokens       1024: 351 us  2048: 332  8192: 316
+        //   64 rows of up to 8192        1024: 191 us  2048: 196  8192: 226
+        //   16 rows of up to 4000         512: 39 us   1024: 40   4096: 59
+        //   1 row of 16000                256: 21 us    512: 20   1024: 24  8192: 111
+        double best = 1e30;
+        for (uint64_t n = 1; n <= kMaxSplits && (n == 1 || tokens > (n / 2) * 256); n *= 2) {
+            const uint64_t part = up(up(tokens, n), 128) * 128;
+            const double each = ((double)part + 128) / 2, units = (double)(n * kv->kv_heads * n_rows) / 256;
+            const double cost = (std::ceil(units) + (n_rows > 1 ? 0.55 * units + 1 : 0)) * each + (n > 1 ? 490 : 0);
+            if (cost < best) best = cost, s.few_part = (uint32_t)part, s.few_splits = (uint32_t)up(tokens, part);
+        }
         if (s.few_splits > 1) s.few_sums = (uint64_t)n_rows * kv->kv_heads * s.few_rows * s.few_splits;
     }
     if (many) {
@@ -255,11 +299,15 @@ int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page
         return hipLaunchKernel(fn, dim3((uint32_t)blocks), dim3(kJoinThreads), args, 0, st) == hipSuccess ? AFX_OK
                                                                                                        : AFX_E_HIP;
     };
-    if (rc == AFX_OK && w.few_sums)
+    const uint32_t teams = kJoinThreads / (a.d / 4);
+    if (rc == AFX_OK && w.few_sums && w.few_splits <= kTeamParts)
+        rc = join(reinterpret_cast<const void *>(&afx_attend_join_teams_kernel),
+                  up((uint64_t)n_rows * a.kv_heads * a.few_rows, teams));
+    else if (rc == AFX_OK && w.few_sums)
         rc = join(reinterpret_cast<const void *>(&afx_attend_join_few_kernel), (uint64_t)n_rows * a.kv_heads * a.few_rows);
     if (rc == AFX_OK && w.many_sums)
         rc = join(reinterpret_cast<const void *>(&afx_attend_join_many_kernel),
-                  up((uint64_t)m * a.q_heads, kJoinThreads / (a.d / 4)));
+                  up((uint64_t)m * a.q_heads, teams));
     return rc;
 }
 

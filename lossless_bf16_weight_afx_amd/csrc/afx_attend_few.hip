@@ -64,157 +64,205 @@ __device__ inline bool odd(u32x4 v) {
     return t & 0x80008000u;
 }
 
-// One pass over the wave's tiles from j0 to j1. kFull: a head has 32 KC
-// dimensions, none of a fragment lies behind them.
+__device__ inline u32x4 once(const uint16_t *p) {  // (read by this wave only)
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+}
+
+// A wave's reads of a tile of 32 tokens. kFull: a head has 32 KC dimensions,
+// none of a fragment lies behind them.
+template <int KC, bool kFull>
+struct Reads {
+    static constexpr int kDT = 2 * KC;
+    const AttendArgs &a;
+    const Where &w;
+    uint32_t c, g;
+
+    // The page ids of the lane's key tokens (8 (c / 4) ..) and value tokens (8 g ..).
+    __device__ uint32_t page(int32_t at) const { return (uint32_t)w.table[min((uint32_t)at >> w.shift, a.max_pages - 1)]; }
+    __device__ uint32_t k_page(int32_t j) const { return page(j + 8 * (int32_t)(c >> 2)); }
+    __device__ uint32_t v_page(int32_t j) const { return page(j + 8 * (int32_t)g); }
+
+    __device__ void keys(int32_t j, uint32_t id, u32x4 (&f)[2][KC]) const {
+        const uint32_t tok = ((uint32_t)j + 8 * (c >> 2) + (c & 3)) & (w.size - 1), last = w.d / 8 - 1;
+        const uint16_t *p = w.k + (uint64_t)(id < a.n_pages ? id : 0) * w.page_elems + tok * 8;
+        if (kFull) p += g * w.size * 8;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+            const uint16_t *pc = p + (kFull ? 4 * kc : min(4 * kc + g, last)) * w.size * 8;
+            f[0][kc] = once(pc);
+            f[1][kc] = once(pc + 32);
+        }
+    }
+    __device__ void values(int32_t j, uint32_t id, u32x4 (&f)[kDT]) const {
+        const uint32_t tok = ((uint32_t)j + 8 * g) & (w.size - 1);
+        const uint16_t *p = w.v + (uint64_t)(id < a.n_pages ? id : 0) * w.page_elems + tok * w.d + (kFull ? c * 8 : 0);
+#pragma unroll
+        for (int t = 0; t < kDT; ++t)
+            f[t] = once(p + (kFull ? 16 * t : min(16 * t + c, w.d - 1)) * 8);
+    }
+};
+
+// The scores of a tile: sc[x][y][e] is that of query row c of group x and token 8 g + 4 y + e.
+template <int KC, int RG, bool kFull>
+__device__ __forceinline__ void scores(const Where &w, const Wave<KC, RG> &s, const u32x4 (&kf)[2][KC], uint32_t g,
+                                       f32x4 (&sc)[RG][2]) {
+#pragma unroll
+    for (int x = 0; x < RG; ++x) sc[x][0] = sc[x][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            u32x4 f = kf[y][kc];
+            if (!kFull && kc >= KC - 2 && 4 * kc + g >= w.d / 8) f = u32x4{0, 0, 0, 0};  // behind the head's dimensions
+#pragma unroll
+            for (int x = 0; x < RG; ++x)
+                sc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), s.q[x][kc], sc[x][y], 0,
+                                                                   0, 0);
+        }
+}
+
+// Their weights, with the running maximum and sum.
+template <int KC, int RG>
+__device__ __forceinline__ void weights(const AttendArgs &a, Wave<KC, RG> &s, const f32x4 (&sc)[RG][2], bf16x8 (&p)[RG]) {
+#pragma unroll
+    for (int x = 0; x < RG; ++x) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = sc[x][e / 4][e % 4];
+        float best = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+        best *= a.scale2;
+        if (__any(best > s.top[x] + kSlack)) {
+            best = fmaxf(best, __shfl_xor(best, 16));
+            best = fmaxf(best, __shfl_xor(best, 32));
+            const float now = fmaxf(s.top[x], best);
+            const float f = now == -INFINITY ? 1.f : exp2_fast(s.top[x] - now);
+            s.top[x] = now;
+            s.sum[x] *= f;
+#pragma unroll
+            for (int t = 0; t < 2 * KC; ++t) s.o[x][t] *= f;
+        }
+        const float base = s.top[x] == -INFINITY ? 0.f : s.top[x];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = exp2_fast(__builtin_fmaf(v[e], a.scale2, -base));
+        s.sum[x] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[x][e] = (__bf16)v[e];
+    }
+}
+
+template <int KC, int RG>
+__device__ __forceinline__ void add_values(Wave<KC, RG> &s, const u32x4 (&vf)[2 * KC], const bf16x8 (&p)[RG]) {
+#pragma unroll
+    for (int t = 0; t < 2 * KC; ++t)
+#pragma unroll
+        for (int x = 0; x < RG; ++x)
+            s.o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf[t]), p[x], s.o[x][t], 0, 0, 0);
+}
+
+// The tile at j, of which some rows see only a part, or not all pages are in the cache.
+template <int KC, int RG, bool kFull>
+__device__ __forceinline__ void partial_tile(const AttendArgs &a, const Where &w, Wave<KC, RG> &s, int32_t j,
+                                             uint32_t lane) {
+    lane = opaque(lane);
+    const uint32_t c = lane & 15, g = lane >> 4;
+    const Reads<KC, kFull> reads{a, w, c, g};
+    const uint32_t id = reads.v_page(j);
+    u32x4 kf[2][KC], vf[2 * KC];
+    reads.keys(j, reads.k_page(j), kf);
+    reads.values(j, id, vf);
+    f32x4 sc[RG][2];
+    scores<KC, RG, kFull>(w, s, kf, g, sc);
+    uint32_t any = 0;  // of the lane's 8 tokens, those that some row sees
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int32_t at = j + 8 * (int32_t)g + e;
+        const bool there = id < a.n_pages;
+        any |= there && at >= w.first && at < w.last ? 1u << e : 0u;
+#pragma unroll
+        for (int x = 0; x < RG; ++x)
+            if (!there || at < s.begin[x] || at >= s.end[x]) sc[x][e / 4][e % 4] = -INFINITY;
+    }
+    bf16x8 p[RG];
+    weights<KC, RG>(a, s, sc, p);
+    bool strange = false;
+#pragma unroll
+    for (int t = 0; t < 2 * KC; ++t) {
+        vf[t] = only(vf[t], any);
+        strange |= odd(vf[t]);
+    }
+    // (a strange one: value by value, so that it reaches only the rows that see it)
+    const int32_t odd_end = __any(strange) ? (int32_t)kFewTokens : 0;
+    if (odd_end == 0) add_values<KC, RG>(s, vf, p);
+#pragma unroll 1
+    for (int e = 0; e < odd_end; ++e) {
+        const int32_t at = j + e;
+        const uint32_t page = __shfl(id, 16 * (e / 8));
+        if (page >= a.n_pages) continue;
+        const uint32_t own = opaque(4 * g);
+        const uint16_t *pv = w.v + (uint64_t)page * w.page_elems + (at & (w.size - 1) & ~7u) * w.d + at % 8 + own * 8;
+#pragma unroll
+        for (int x = 0; x < RG; ++x) {
+            const u32x4 bits = __builtin_bit_cast(u32x4, p[x]);
+            const uint32_t two = e / 2 % 4 == 0 ? bits[0] : e / 2 % 4 == 1 ? bits[1] : e / 2 % 4 == 2 ? bits[2] : bits[3];
+            const uint32_t got = __shfl(two, c + 16 * (e / 8));
+            const bool seen = at >= s.begin[x] && at < s.end[x];
+            const float weight = from_bf16((uint16_t)(e % 2 ? got >> 16 : got));
+#pragma unroll
+            for (int t = 0; t < 2 * KC; ++t) {
+                float v[4] = {};
+                if (kFull || 16 * t + own < w.d) {  // (d is a multiple of 8: all four or none)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = from_bf16(pv[(16 * t + r) * 8]);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s.o[x][t][r] = seen ? s.o[x][t][r] + weight * v[r] : s.o[x][t][r];
+            }
+        }
+    }
+}
+
+// One pass over the wave's tiles from j0 to j1.
 template <int KC, int RG, bool kFull>
 __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC, RG> &s, int32_t j0, int32_t j1,
                                     uint32_t wave, uint32_t lane) {
-    constexpr int kDT = 2 * KC;
-    const uint32_t c = lane & 15, g = lane >> 4;
-    const uint32_t chunks = w.d / 8;
 #pragma unroll
     for (int x = 0; x < RG; ++x) {
         s.top[x] = -INFINITY;
         s.sum[x] = 0.f;
 #pragma unroll
-        for (int t = 0; t < kDT; ++t) s.o[x][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 2 * KC; ++t) s.o[x][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    int32_t j = j0 + (int32_t)(wave * kFewTokens);
-    if (j >= j1) return;
-    // page ids of the lane's key tokens (8 (c / 4) ..) and value tokens (8 g ..)
-    auto page_of = [&](int32_t at) {
-        return (uint32_t)w.table[min((uint32_t)at >> w.shift, a.max_pages - 1)];
-    };
-    u32x4 kf[2][KC], vf[kDT];
-    auto load_k = [&](int32_t at, uint32_t id) {
-        const uint32_t tok = (uint32_t)at + 8 * (c >> 2) + (c & 3);
-        const uint16_t *p = w.k + (uint64_t)(id < a.n_pages ? id : 0) * w.page_elems + (tok & (w.size - 1)) * 8;
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-            const uint32_t chunk = 4 * kc + g;
-            const uint16_t *pc = p + (kFull ? chunk : min(chunk, chunks - 1)) * w.size * 8;
-            kf[0][kc] = *reinterpret_cast<const u32x4 *>(pc);
-            kf[1][kc] = *reinterpret_cast<const u32x4 *>(pc + 32);
-        }
-    };
-    auto load_v = [&](int32_t at, uint32_t id) {
-        const uint32_t tok = ((uint32_t)at + 8 * g) & (w.size - 1);
-        const uint16_t *p = w.v + (uint64_t)(id < a.n_pages ? id : 0) * w.page_elems + tok * w.d;
-#pragma unroll
-        for (int t = 0; t < kDT; ++t)
-            vf[t] = *reinterpret_cast<const u32x4 *>(p + (kFull ? 16 * t + c : min(16 * t + c, w.d - 1)) * 8);
-    };
     constexpr int32_t kStep = kWaves * kFewTokens;
-    uint32_t kid = page_of(j + 8 * (c >> 2)), vid = page_of(j + 8 * g);
-    uint32_t kid2 = page_of(j + kStep + 8 * (c >> 2)), vid2 = page_of(j + kStep + 8 * g);
-    load_k(j, kid);
-    load_v(j, vid);
-    for (; j < j1; j += kStep) {
-        f32x4 sc[RG][2];
-#pragma unroll
-        for (int x = 0; x < RG; ++x) sc[x][0] = sc[x][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                u32x4 f = kf[y][kc];
-                if (!kFull && kc >= KC - 2 && 4 * kc + g >= chunks) f = u32x4{0, 0, 0, 0};  // behind the head's dimensions
-#pragma unroll
-                for (int x = 0; x < RG; ++x)
-                    sc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), s.q[x][kc],
-                                                                       sc[x][y], 0, 0, 0);
+    const uint32_t g = lane >> 4;
+    const Reads<KC, kFull> reads{a, w, lane & 15, g};
+    int32_t j = j0 + (int32_t)(wave * kFewTokens);
+    const int32_t end = min(w.hi - (int32_t)kFewTokens, j1 - 1);  // the last place of a whole tile
+    while (j < j1) {
+        if (j >= w.lo && j <= end) {
+            uint32_t id = reads.v_page(j), kid2 = reads.k_page(j + kStep), vid2 = reads.v_page(j + kStep);
+            u32x4 kf[2][KC], vf[2 * KC];
+            reads.keys(j, reads.k_page(j), kf);
+            reads.values(j, id, vf);
+            while (__all(id < a.n_pages)) {
+                f32x4 sc[RG][2];
+                scores<KC, RG, kFull>(w, s, kf, g, sc);
+                const uint32_t kid3 = reads.k_page(j + 2 * kStep), vid3 = reads.v_page(j + 2 * kStep);
+                const bool more = j + kStep <= end;
+                if (more) reads.keys(j + kStep, kid2, kf);
+                bf16x8 p[RG];
+                weights<KC, RG>(a, s, sc, p);
+                add_values<KC, RG>(s, vf, p);
+                j += kStep;
+                if (!more) break;
+                reads.values(j, vid2, vf);
+                id = vid2;
+                kid2 = kid3;
+                vid2 = vid3;
             }
-        const uint32_t id = vid;
-        const bool more = j + kStep < j1;
-        const uint32_t kid3 = page_of(j + 2 * kStep + 8 * (c >> 2)), vid3 = page_of(j + 2 * kStep + 8 * g);
-        if (more) load_k(j + kStep, kid2);
-        const bool clean = j >= w.lo && j + (int32_t)kFewTokens <= w.hi && __all(id < a.n_pages);
-        uint32_t any = 0xFF;  // of the lane's 8 tokens, those that some row sees
-        if (!clean) {
-            any = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int32_t at = j + 8 * (int32_t)g + e;
-                any |= id < a.n_pages && at >= w.first && at < w.last ? 1u << e : 0u;
-            }
+            if (j > end) continue;
         }
-        bf16x8 p[RG];
-#pragma unroll
-        for (int x = 0; x < RG; ++x) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = sc[x][e / 4][e % 4];
-            if (!clean) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int32_t at = j + 8 * (int32_t)g + e;
-                    if (id >= a.n_pages || at < s.begin[x] || at >= s.end[x]) v[e] = -INFINITY;
-                }
-            }
-            float best = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-            best *= a.scale2;
-            if (__any(best > s.top[x] + kSlack)) {
-                best = fmaxf(best, __shfl_xor(best, 16));
-                best = fmaxf(best, __shfl_xor(best, 32));
-                const float now = fmaxf(s.top[x], best);
-                const float f = now == -INFINITY ? 1.f : exp2_fast(s.top[x] - now);
-                s.top[x] = now;
-                s.sum[x] *= f;
-#pragma unroll
-                for (int t = 0; t < kDT; ++t) s.o[x][t] *= f;
-            }
-            const float base = s.top[x] == -INFINITY ? 0.f : s.top[x];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = exp2_fast(__builtin_fmaf(v[e], a.scale2, -base));
-            s.sum[x] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[x][e] = (__bf16)v[e];
-        }
-        bool strange = false;
-        if (!clean) {
-#pragma unroll
-            for (int t = 0; t < kDT; ++t) {
-                vf[t] = only(vf[t], any);
-                strange |= odd(vf[t]);
-            }
-        }
-        if (!clean && __any(strange)) {
-            // value by value, so that an infinity or NaN reaches only the rows that see it
-            const uint32_t dims = opaque(w.d), own = opaque(4 * g);
-#pragma unroll 1
-            for (int e = 0; e < (int)kFewTokens; ++e) {
-                const int32_t at = j + e;
-                const uint32_t page = __shfl(id, 16 * (e / 8));
-                if (page >= a.n_pages) continue;
-                const uint16_t *pv = w.v + (uint64_t)page * w.page_elems + (at & (w.size - 1) & ~7u) * dims + at % 8;
-#pragma unroll
-                for (int x = 0; x < RG; ++x) {
-                    const u32x4 bits = __builtin_bit_cast(u32x4, p[x]);
-                    const uint32_t two = e / 2 % 4 == 0 ? bits[0] : e / 2 % 4 == 1 ? bits[1] : e / 2 % 4 == 2 ? bits[2] : bits[3];
-                    const uint32_t got = __shfl(two, c + 16 * (e / 8));
-                    const float weight = from_bf16((uint16_t)(e % 2 ? got >> 16 : got));
-                    if (at >= s.begin[x] && at < s.end[x])
-#pragma unroll
-                        for (int t = 0; t < kDT; ++t)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const uint32_t dim = 16 * t + own + r;
-                                if (dim < dims) s.o[x][t][r] += weight * from_bf16(pv[dim * 8]);
-                            }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < kDT; ++t)
-#pragma unroll
-                for (int x = 0; x < RG; ++x)
-                    s.o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf[t]), p[x], s.o[x][t],
-                                                                        0, 0, 0);
-        }
-        if (more) load_v(j + kStep, vid2);
-        vid = vid2;
-        kid2 = kid3;
-        vid2 = vid3;
+        if (j < j1) partial_tile<KC, RG, kFull>(a, w, s, j, lane);
+        j += kStep;
     }
 }
 
