@@ -23,8 +23,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kFewTokens = 32;    // tokens of a wave's tile in the kernel for few query rows
-constexpr uint32_t kManyRows = 128;    // query rows of a workgroup in the kernel for many
-constexpr uint32_t kManyTokens = 64;   // and tokens of its tile
+// Waves of 32 query rows of a workgroup in the kernel for many, by a head's
+// dimensions in units of 32: two on a SIMD while their registers allow it.
+constexpr uint32_t many_waves(int kc) { return kc <= 4 ? 8 : 4; }
 constexpr uint32_t kMaxSplits = 256;   // parts that a row's tokens are cut into
 
 struct AttendArgs {

@@ -182,13 +182,13 @@ Plan plan(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t
         if (s.few_splits > 1) s.few_sums = (uint64_t)n_rows * kv->kv_heads * s.few_rows * s.few_splits;
     }
     if (many) {
-        const uint64_t tiles = up((uint64_t)m * group, kManyRows);
-        s.many_tiles = (uint32_t)((uint64_t)m * group / kManyRows + n_rows);
-        // whole rounds of two workgroups a CU, parts of 256 tokens at least
+        const uint64_t rows = 32 * many_waves((int)up(kv->head_dim, 32)), tiles = up((uint64_t)m * group, rows);
+        s.many_tiles = (uint32_t)((uint64_t)m * group / rows + n_rows);
+        // whole rounds of one workgroup a CU, parts of 256 tokens at least
         const uint64_t most_splits = std::min<uint64_t>(16, std::max<uint64_t>(1, tokens / 256));
         double best = 1e30;
         for (uint64_t n = 1; n <= most_splits; ++n) {
-            const double cost = (double)up(tiles * kv->kv_heads * n, 512) / (double)n * (1 + 0.02 * (double)(n - 1));
+            const double cost = (double)up(tiles * kv->kv_heads * n, 256) / (double)n * (1 + 0.02 * (double)(n - 1));
             if (cost < best * 0.98) best = cost, s.many_splits = (uint32_t)n;
         }
         if (s.many_splits > 1) s.many_sums = (uint64_t)m * p->q_heads * s.many_splits;

@@ -1,18 +1,26 @@
 // afx_attend_many.hip -- attention of many query rows (chunks of prompts) over
 // a paged cache (gfx950).
 //
-// The matrix cores bound it. A workgroup of 4 waves takes 128 query rows of
-// one key-value head, 32 a wave, and its keys and values in tiles of 64
-// tokens, which go from the pages to LDS without passing through registers
-// and are double-buffered: the next tile is requested right after the barrier
-// that frees its buffer. The pages' order is that of the operands, so that
+// The matrix cores bound it, with the vector unit close behind: 32 tokens of a
+// wave's 32 rows are 16 matrix instructions of 32 cycles and 16 exponentials
+// of 16. A workgroup of 8 waves takes 256 query rows of one key-value head, 32
+// a wave, and its keys and values in tiles of 64 tokens (heads of more than
+// 128 dimensions: 4 waves, tiles of 32), which go from the pages to LDS without
+// passing through registers. The pages' order is that of the operands, so that
 // every LDS read is 16 bytes a lane, 512 in a row.
 //   S^T = K Q^T    v_mfma_f32_32x32x16_bf16, K rows (tokens) as A, query rows
-//                  as B: a lane holds 32 tokens' scores of one query row;
+//                  as B: a lane holds 16 of 32 tokens' scores of one query row;
 //   O^T += V^T P^T V^T rows (dimensions) as A, the weights as B.
 // Rows 4 .. 7 and 8 .. 11 of every 16 score rows take each other's tokens, so
 // that a half wave ends up with the scores of tokens 8 h .. 8 h + 7 of every
-// 16, which is what it has to feed as B. The running maximum moves only when a
+// 16, which is what it has to feed as B.
+//
+// A wave runs one step of 32 tokens ahead of itself: while the vector unit
+// forms one step's weights, the matrix cores multiply the next step's keys,
+// and its largest score is found while they multiply the first step's values.
+// Its keys thus belong to the next tile at a tile's last step, where the
+// barrier stands; three tiles of LDS let the tile after that be requested
+// there, with a tile's time to arrive. The running maximum moves only when a
 // score exceeds it by 8 (a factor 2^8), as in afx_attend_few.hip.
 #include <type_traits>
 
@@ -21,9 +29,18 @@
 namespace afx {
 namespace {
 
-constexpr uint32_t kWaves = 4, kThreads = 64 * kWaves;
 constexpr float kSlack = 8.f;
-constexpr uint32_t kT = kManyTokens;
+
+template <int KC>
+struct Shape {
+    static constexpr uint32_t kWaves = many_waves(KC), kThreads = 64 * kWaves, kRows = 32 * kWaves;
+    static constexpr uint32_t kT = KC <= 4 ? 64 : 32;  // tokens of a tile
+    static constexpr int kSteps = kT / 32;
+    static constexpr uint32_t kDims = 32 * KC;
+    static constexpr uint32_t kBytes = kT * kDims * 2;  // of a key tile, [dim / 8][token] of 16, or value tile, [token / 8][dim]
+    static constexpr uint32_t kPieces = kBytes / 1024;  // a wave's load fills 1 KB
+    static constexpr int kEach = (kPieces + kWaves - 1) / kWaves;
+};
 
 // 16 bytes a lane from p into LDS at `to` (wave-uniform) + 16 lane.
 __device__ inline void load_to_lds(const uint16_t *p, uint8_t *to) {
@@ -39,7 +56,7 @@ struct Tile {
 
 // Tile number u, counted over the batch rows that this kernel takes, the last
 // tiles of a row (the longest) first. False behind the last.
-__device__ inline bool find_tile(const AttendArgs &a, uint32_t u, Tile &t) {
+__device__ inline bool find_tile(const AttendArgs &a, uint32_t u, uint32_t rows, Tile &t) {
     const uint32_t lane = threadIdx.x % 64;
     uint32_t before = 0;
     for (uint32_t r0 = 0; r0 < a.n_rows; r0 += 64) {
@@ -50,7 +67,7 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t u, Tile &t) {
             const uint32_t to = (uint32_t)min(max(a.starts[r + 1], 0), (int32_t)a.m);
             n = to > from ? (to - from) * a.group : 0;
         }
-        const uint32_t tiles = n > a.few_rows ? (n + kManyRows - 1) / kManyRows : 0;
+        const uint32_t tiles = n > a.few_rows ? (n + rows - 1) / rows : 0;
         uint32_t sum = tiles;
 #pragma unroll
         for (uint32_t o = 1; o < 64; o *= 2) {
@@ -63,7 +80,7 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t u, Tile &t) {
             t.row = BatchRow(a, __builtin_amdgcn_readfirstlane(r0 + l));
             t.rows = t.row.n * a.group;
             const uint32_t end = before + __builtin_amdgcn_readlane(sum, l);
-            t.r0 = (end - 1 - u) * kManyRows;
+            t.r0 = (end - 1 - u) * rows;
             return true;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
@@ -71,13 +88,10 @@ __device__ inline bool find_tile(const AttendArgs &a, uint32_t u, Tile &t) {
     return false;
 }
 
-// Bytes of a key tile, [dim / 8][token] of 16, and of a value tile, [token / 8][dim] of 16.
-constexpr uint32_t tile_bytes(int KC) { return 32 * KC / 8 * kT * 16; }
-
 template <int KC>
 struct Wave {
     bf16x8 q[2 * KC];
-    f32x16 o[KC];
+    f32x16 o[KC], sc;  // outputs; the scores of the next step
     float top, sum;
     int32_t begin, end;  // positions that the lane's row sees
 };
@@ -92,189 +106,279 @@ struct Where {
     int32_t wg_first, wg_last;
 };
 
-// The tile at position j, which lies in k_tile and v_tile; there: its tokens
-// whose pages are in the cache.
+// The largest of the lane's scores.
+__device__ inline float largest(const f32x16 &s) {
+    float best = fmaxf(s[0], s[1]);
+#pragma unroll
+    for (int e = 2; e < 16; e += 2) best = fmaxf(best, fmaxf(s[e], s[e + 1]));
+    return best;
+}
+
+// Moves the running maximum to the scores of the next step, where one exceeds it by kSlack.
 template <int KC>
-__device__ __forceinline__ void use_tile(const AttendArgs &a, const Where &w, Wave<KC> &s, uint8_t *k_tile,
-                                         uint8_t *v_tile, int32_t j, uint64_t there, uint32_t lane) {
-    constexpr uint32_t kDims = 32 * KC;
+__device__ __forceinline__ void follow(Wave<KC> &s, float best) {
+    if (!__any(best > s.top + kSlack)) return;
+    best = fmaxf(best, __shfl_xor(best, 32));
+    const float now = fmaxf(s.top, best);
+    const float f = now == -INFINITY ? 1.f : exp2_fast(s.top - now);
+    s.top = now;
+    s.sum *= f;
+#pragma unroll
+    for (int t = 0; t < KC; ++t) s.o[t] *= f;
+}
+
+// Without the scores of what the lane's row does not see; j: the step's first
+// position, there: which of its 32 tokens have pages in the cache.
+template <int KC>
+__device__ __forceinline__ void hide(Wave<KC> &s, int32_t j, uint32_t there, uint32_t lane) {
+    // the lane's tokens of e: 8 h + t, t = 16 (e / 8) + e mod 8
+    const uint32_t h8 = opaque(lane) >> 5 << 3;
+    const int32_t own = j + (int32_t)h8;
+    const uint32_t from = (uint32_t)max(s.begin - own, 0), n = (uint32_t)max(s.end - own - (int32_t)from, 0);
+    const uint32_t pages = there >> h8;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const uint32_t t = 16 * (e / 8) + e % 8;
+        if (t - from >= n || !(pages >> t & 1)) s.sc[e] = -INFINITY;
+    }
+}
+
+// Values of the tile at j that no row of the workgroup sees become 0; whether
+// the others hold an infinity or NaN. there: which tokens have pages.
+template <int KC>
+__device__ __forceinline__ bool clear_values(const Where &w, uint8_t *v_tile, int32_t j, uint64_t there) {
+    using S = Shape<KC>;
+    uint32_t odd = 0;
+    for (uint32_t x = opaque(threadIdx.x); x < S::kBytes / 16; x += S::kThreads) {
+        u32x4 *p = reinterpret_cast<u32x4 *>(v_tile + x * 16);
+        u32x4 v = *p;
+        const uint32_t t8 = x / S::kDims * 8;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            auto seen = [&](uint32_t t) {
+                const int32_t at = j + (int32_t)t;
+                return (there >> t & 1) && at >= w.wg_first && at < w.wg_last;
+            };
+            v[e] &= (seen(t8 + 2 * e) ? 0xFFFFu : 0u) | (seen(t8 + 2 * e + 1) ? 0xFFFF0000u : 0u);
+            odd |= (v[e] & 0x7F807F80u) + 0x00800080u;  // (only all ones carry into bit 15)
+        }
+        *p = v;
+    }
+    return __syncthreads_or((odd & 0x80008000u) != 0);
+}
+
+// A step's values one by one, so that an infinity or NaN reaches only the
+// rows that see it.
+template <int KC>
+__device__ __forceinline__ void add_strange(Wave<KC> &s, bf16x8 p0, bf16x8 p1, const uint8_t *v_step, int32_t j,
+                                            uint32_t there, uint32_t lane) {
+    const uint32_t i = opaque(lane) & 31, own = opaque(lane) >> 5 << 2;
+    const u32x4 b0 = __builtin_bit_cast(u32x4, p0), b1 = __builtin_bit_cast(u32x4, p1);
+#pragma unroll 1
+    for (uint32_t t = 0; t < 32; ++t) {
+        const uint32_t x = t / 2 % 4;
+        const uint32_t two = t < 16 ? x == 0 ? b0[0] : x == 1 ? b0[1] : x == 2 ? b0[2] : b0[3]
+                                    : x == 0 ? b1[0] : x == 1 ? b1[1] : x == 2 ? b1[2] : b1[3];
+        const uint32_t got = __shfl(two, i + 32 * (t / 8 % 2));
+        const float weight = from_bf16((uint16_t)(t % 2 ? got >> 16 : got));
+        const int32_t at = j + (int32_t)t;
+        const bool seen = (there >> t & 1) && at >= s.begin && at < s.end;
+        const uint16_t *values = reinterpret_cast<const uint16_t *>(v_step) + (t / 8 * 32 * KC + own) * 8 + t % 8;
+#pragma unroll
+        for (int d = 0; d < KC; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float v = from_bf16(values[(32 * d + (e & 3) + 8 * (e >> 2)) * 8]);
+                s.o[d][e] = seen ? s.o[d][e] + weight * v : s.o[d][e];
+            }
+    }
+}
+
+// The keys of step n of a tile: s.sc.
+template <int KC>
+__device__ __forceinline__ void multiply_keys(Wave<KC> &s, const uint8_t *k_tile, int n, uint32_t lane) {
+    using S = Shape<KC>;
     const uint32_t i = lane & 31, h = lane >> 5;
     // a score row's token: rows 4 .. 7 and 8 .. 11 of 16 change places
     const uint32_t tok = (i & 16) | (i & 3) | ((i & 4) << 1) | ((i & 8) >> 1);
-    bool strange = false;
-    if (there != ~0ull || j < w.wg_lo || j + (int32_t)kT > w.wg_hi) {
-        // A tile that some rows see in part: values of tokens that none sees become 0, and infinities and NaN
-        // among the others are looked for.
-        for (uint32_t x = threadIdx.x; x < 8 * kDims; x += kThreads) {
-            u32x4 *p = reinterpret_cast<u32x4 *>(v_tile + x * 16);
-            u32x4 v = *p;
-            const uint32_t t8 = x / kDims * 8;
-            uint32_t odd = 0;
+    const uint8_t *base = k_tile + (h * S::kT + tok) * 16;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                auto seen = [&](uint32_t t) {
-                    const int32_t at = j + (int32_t)t;
-                    return (there >> t & 1) && at >= w.wg_first && at < w.wg_last;
-                };
-                v[e] &= (seen(t8 + 2 * e) ? 0xFFFFu : 0u) | (seen(t8 + 2 * e + 1) ? 0xFFFF0000u : 0u);
-                odd |= (v[e] & 0x7F807F80u) + 0x00800080u;  // (only all ones carry into bit 15)
-            }
-            strange |= (odd & 0x80008000u) != 0;
-            *p = v;
-        }
-        strange = __syncthreads_or(strange);
-    }
-    if (j >= w.last || j + (int32_t)kT <= w.first) return;  // no row of this wave sees the tile
-    f32x16 sc[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sc[x][e] = 0.f;
+    for (int e = 0; e < 16; ++e) s.sc[e] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < 2 * KC; ++ks)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const bf16x8 f = *reinterpret_cast<const bf16x8 *>(k_tile + ((2 * ks + h) * kT + 32 * x + tok) * 16);
-            sc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, s.q[ks], sc[x], 0, 0, 0);
-        }
-    const bool clean = there == ~0ull && j >= w.lo && j + (int32_t)kT <= w.hi;
-    if (!clean) {
-        // the lane's tokens of x, e: 8 h + t, t = 32 x + 16 (e / 8) + e mod 8
-        const int32_t own = j + 8 * (int32_t)h;
-        const uint32_t from = (uint32_t)max(s.begin - own, 0), n = (uint32_t)max(s.end - own - (int32_t)from, 0);
-        const uint64_t pages = there >> (8 * h);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t t = 32 * x + 16 * (e / 8) + e % 8;
-                if (t - from >= n || !(pages >> t & 1)) sc[x][e] = -INFINITY;
-            }
-    }
-    float best = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) best = fmaxf(best, fmaxf(sc[0][e], sc[1][e]));
-    best *= a.scale2;
-    if (__any(best > s.top + kSlack)) {
-        best = fmaxf(best, __shfl_xor(best, 32));
-        const float now = fmaxf(s.top, best);
-        const float f = now == -INFINITY ? 1.f : exp2_fast(s.top - now);
-        s.top = now;
-        s.sum *= f;
-#pragma unroll
-        for (int t = 0; t < KC; ++t) s.o[t] *= f;
-    }
-    const float base = s.top == -INFINITY ? 0.f : s.top;
-    bf16x8 p[4];
-    float part[4] = {};
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float v = exp2_fast(__builtin_fmaf(sc[x][e], a.scale2, -base));
-            part[e % 4] += v;
-            p[2 * x + e / 8][e % 8] = (__bf16)v;
-        }
-    s.sum += (part[0] + part[1]) + (part[2] + part[3]);
-    if (strange) {
-        // value by value, so that an infinity or NaN reaches only the rows that see it
-        const uint32_t own = opaque(4 * h);
-#pragma unroll 1
-        for (uint32_t t = 0; t < kT; ++t) {
-            const u32x4 bits = t / 16 == 0   ? __builtin_bit_cast(u32x4, p[0])
-                               : t / 16 == 1 ? __builtin_bit_cast(u32x4, p[1])
-                               : t / 16 == 2 ? __builtin_bit_cast(u32x4, p[2])
-                                             : __builtin_bit_cast(u32x4, p[3]);
-            const uint32_t two = t / 2 % 4 == 0 ? bits[0] : t / 2 % 4 == 1 ? bits[1] : t / 2 % 4 == 2 ? bits[2] : bits[3];
-            const uint32_t got = __shfl(two, i + 32 * (t / 8 % 2));
-            const float weight = from_bf16((uint16_t)(t % 2 ? got >> 16 : got));
-            const int32_t at = j + (int32_t)t;
-            if (!(there >> t & 1) || at < s.begin || at >= s.end) continue;
-            const uint16_t *values = reinterpret_cast<const uint16_t *>(v_tile) + t / 8 * kDims * 8 + t % 8;
-#pragma unroll
-            for (int d = 0; d < KC; ++d)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint32_t dim = 32 * d + (e & 3) + 8 * (e >> 2) + own;
-                    s.o[d][e] += weight * from_bf16(values[dim * 8]);
-                }
-        }
-        return;
-    }
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int d = 0; d < KC; ++d) {
-            const bf16x8 f = *reinterpret_cast<const bf16x8 *>(v_tile + ((2 * ks + h) * kDims + 32 * d + i) * 16);
-            s.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p[ks], s.o[d], 0, 0, 0);
-        }
+        s.sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            *reinterpret_cast<const bf16x8 *>(base + (2 * ks * S::kT + 32 * n) * 16), s.q[ks], s.sc, 0, 0, 0);
 }
 
-// All tiles from j0 to j1. The four buffers are objects of their own: of one
-// array the compiler would have every read wait for all loads into it.
+// One step: the weights of s.sc, which are of step n of the tile at j, times
+// the step's values, and the scores of the next step (step m of `next`).
+template <int KC>
+__device__ __forceinline__ void step(const AttendArgs &a, const Where &w, Wave<KC> &s, const uint8_t *v_tile, int n,
+                                     const uint8_t *next, int m, bool more, int32_t j, int32_t j_next, bool strange,
+                                     uint32_t there, uint32_t there_next, uint32_t lane) {
+    using S = Shape<KC>;
+    const uint32_t i = lane & 31, h = lane >> 5;
+    const float base = s.top == -INFINITY ? 0.f : s.top;
+    bf16x8 p[2];
+    auto weigh = [&](const f32x16 &was) __attribute__((always_inline)) {
+        float part[4] = {};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float v = exp2_fast(__builtin_fmaf(was[e], a.scale2, -base));
+            part[e % 4] += v;
+            p[e / 8][e % 8] = (__bf16)v;
+        }
+        s.sum += (part[0] + part[1]) + (part[2] + part[3]);
+    };
+    float best;
+    if (!strange) {
+        const f32x16 was = s.sc;
+        const uint8_t *v_base = v_tile + ((4 * n + h) * S::kDims + i) * 16;
+        bf16x8 v[2 * KC];
+        // the next step's keys beside this one's weights
+        multiply_keys<KC>(s, next, m, lane);
+        weigh(was);
+#pragma unroll
+        for (int x = 0; x < 2 * KC; ++x)
+            v[x] = *reinterpret_cast<const bf16x8 *>(v_base + (x / KC * 2 * S::kDims + 32 * (x % KC)) * 16);
+        // and its largest score beside this one's values
+#pragma unroll
+        for (int x = 0; x < 2 * KC; ++x)
+            s.o[x % KC] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[x], p[x / KC], s.o[x % KC], 0, 0, 0);
+        best = largest(s.sc);
+    } else {
+        weigh(s.sc);
+        add_strange<KC>(s, p[0], p[1], v_tile + 4 * n * S::kDims * 16, j, there, lane);
+        multiply_keys<KC>(s, next, m, opaque(lane));
+        best = largest(s.sc);
+    }
+    if (there_next != ~0u || j_next < w.lo || j_next + 32 > w.hi) {
+        hide<KC>(s, j_next, there_next, lane);
+        best = largest(s.sc);
+    }
+    follow<KC>(s, more ? best * a.scale2 : -INFINITY);
+}
+
+// All tiles from j0 to j1. The buffers are objects of their own: of one array
+// the compiler would have every read wait for all loads into it.
 template <int KC>
 __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC> &s, uint8_t *k0, uint8_t *v0,
-                                    uint8_t *k1, uint8_t *v1, int32_t j0, int32_t j1, uint32_t wave, uint32_t lane) {
-    constexpr uint32_t kDims = 32 * KC;
-    const uint32_t pieces = a.d / 8;
+                                    uint8_t *k1, uint8_t *v1, uint8_t *k2, uint8_t *v2, int32_t j0, int32_t j1,
+                                    uint32_t wave, uint32_t lane) {
+    using S = Shape<KC>;
+    constexpr int32_t kT = S::kT;
+    const uint32_t chunks = a.d / 8;
     s.top = -INFINITY;
     s.sum = 0.f;
 #pragma unroll
     for (int t = 0; t < KC; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s.o[t][e] = 0.f;
-    auto page_of = [&](int32_t at) {  // of the lane's token of the tile at `at`
-        return (uint32_t)w.table[min(((uint32_t)at + lane) >> a.page_shift, a.max_pages - 1)];
+    if (j0 >= j1) return;
+    auto page_of = [&](int32_t at) __attribute__((always_inline)) {  // of the lane's token of the tile at `at`
+        return (uint32_t)w.table[min(((uint32_t)at + lane % kT) >> a.page_shift, a.max_pages - 1)];
     };
-    // Wave w takes 1 KB pieces w, w + 4, .. of both tiles: 8 dimensions of 64 keys, 64 dimensions of 8 values (two
-    // groups of 8 where a head's dimensions end inside a piece). Values behind the head's dimensions repeat its last.
-    auto request = [&](int32_t at, uint32_t id, uint8_t *k_tile, uint8_t *v_tile) {
-        const uint32_t safe = id < a.n_pages ? id : 0;
-        const uint16_t *pk = w.k + (uint64_t)safe * w.page_elems + (((uint32_t)at + lane) & (w.size - 1)) * 8;
-#pragma unroll
-        for (int x = 0; x < KC; ++x) {
-            const uint32_t piece = wave + kWaves * x;
-            if (piece < pieces) load_to_lds(pk + piece * w.size * 8, k_tile + piece * 1024);
-        }
-#pragma unroll
-        for (int x = 0; x < KC; ++x) {
-            const uint32_t entry = (wave + kWaves * x) * 64 + lane, tok = entry / kDims * 8;
-            const uint32_t page = __shfl(safe, tok);
-            load_to_lds(w.v + (uint64_t)page * w.page_elems +
-                            ((((uint32_t)at + tok) & (w.size - 1)) * a.d + min(entry % kDims, a.d - 1) * 8),
-                        v_tile + (wave + kWaves * x) * 1024);
-        }
-    };
-    uint32_t id = page_of(j0), id2 = page_of(j0 + kT);
-    __syncthreads();  // (the keys' zeros)
-    if (j0 < j1) request(j0, id, k0, v0);
-    auto step = [&](int32_t j, uint8_t *k_tile, uint8_t *v_tile, uint8_t *k_next, uint8_t *v_next) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's loads have landed; then every wave's
-        __syncthreads();
-        const uint32_t id3 = page_of(j + 2 * kT);
-        if (j + (int32_t)kT < j1) request(j + kT, id2, k_next, v_next);
+    auto tokens_there = [&](uint32_t id) __attribute__((always_inline)) {
         const uint64_t there = __ballot(id < a.n_pages);
-        id = id2;
-        id2 = id3;
-        use_tile<KC>(a, w, s, k_tile, v_tile, j, there, lane);
+        return kT == 64 ? there : there | ~0ull << 32;
     };
-    for (int32_t j = j0; j < j1; j += 2 * kT) {
-        step(j, k0, v0, k1, v1);
-        if (j + (int32_t)kT < j1) step(j + kT, k1, v1, k0, v0);
+    // Wave w takes 1 KB pieces w, w + kWaves, .. of both tiles: 64 / kT groups of 8 dimensions of kT keys, 64
+    // dimensions of 8 values (of 96 dimensions, two such groups where they end inside a piece). Values behind the
+    // head's dimensions repeat its last.
+    auto request = [&](int32_t at, uint32_t id, uint8_t *k_tile, uint8_t *v_tile) __attribute__((always_inline)) {
+        const uint32_t safe = id < a.n_pages ? id : 0, mask = w.size - 1;
+        const uint16_t *pk = w.k + (uint64_t)safe * w.page_elems + (((uint32_t)at + lane % kT) & mask) * 8;
+#pragma unroll
+        for (int x = 0; x < S::kEach; ++x) {
+            const uint32_t piece = wave + S::kWaves * x;
+            if (S::kPieces % S::kWaves && piece >= S::kPieces) continue;
+            if constexpr (kT == 64) {
+                if (piece < chunks) load_to_lds(pk + piece * w.size * 8, k_tile + piece * 1024);
+            } else {
+                const uint32_t chunk = 2 * piece + lane / 32;  // (a last one behind the head's is loaded twice)
+                if (2 * piece < chunks) load_to_lds(pk + min(chunk, chunks - 1) * w.size * 8, k_tile + piece * 1024);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < S::kEach; ++x) {
+            const uint32_t piece = wave + S::kWaves * x;
+            if (S::kPieces % S::kWaves && piece >= S::kPieces) continue;
+            uint32_t tok, dim, page;
+            if constexpr (S::kDims % 64 == 0) {  // one group of 8 values: its page is the same for all lanes
+                tok = piece / (S::kDims / 64) * 8;
+                dim = piece % (S::kDims / 64) * 64 + lane;
+                page = __builtin_amdgcn_readlane(safe, tok);
+            } else {
+                const uint32_t entry = piece * 64 + lane;
+                tok = entry / S::kDims * 8;
+                dim = entry % S::kDims;
+                page = __shfl(safe, tok);
+            }
+            load_to_lds(w.v + (uint64_t)page * w.page_elems + (((uint32_t)at + tok) & mask) * a.d + min(dim, a.d - 1) * 8,
+                        v_tile + piece * 1024);
+        }
+    };
+    auto whole = [&](int32_t j, uint64_t there) __attribute__((always_inline)) { return there == ~0ull && j >= w.wg_lo && j + kT <= w.wg_hi; };
+    // ids of three tiles: this one's, whose keys and values have arrived, the next one's, which are on their way, and
+    // the one after that
+    uint32_t id = page_of(j0), id1 = page_of(j0 + kT), id2 = page_of(j0 + 2 * kT);
+    __syncthreads();  // (the keys' zeros)
+    request(j0, id, k0, v0);
+    if (j0 + kT < j1) request(j0 + kT, id1, k1, v1);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __syncthreads();
+    uint64_t there = tokens_there(id);
+    bool strange = false;
+    if (!whole(j0, there)) strange = clear_values<KC>(w, v0, j0, there);
+    multiply_keys<KC>(s, k0, 0, lane);
+    if ((uint32_t)there != ~0u || j0 < w.lo || j0 + 32 > w.hi) hide<KC>(s, j0, (uint32_t)there, lane);
+    follow<KC>(s, largest(s.sc) * a.scale2);
+    auto tile = [&](int32_t j, uint8_t *k_tile, uint8_t *v_tile, uint8_t *k_next, uint8_t *v_next, uint8_t *k_after,
+                    uint8_t *v_after) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n + 1 < S::kSteps; ++n)
+            step<KC>(a, w, s, v_tile, n, k_tile, n + 1, true, j + 32 * n, j + 32 * (n + 1), strange,
+                     (uint32_t)(there >> 32 * n), (uint32_t)(there >> 32 * (n + 1)), lane);
+        // The last step multiplies the next tile's keys: it has to have arrived, in every wave. No wave is still in the
+        // tile before this one, whose buffers take the tile after the next.
+        const bool more = j + kT < j1;
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        __syncthreads();
+        const uint64_t there1 = tokens_there(id1);
+        const uint32_t id3 = page_of(j + 3 * kT);
+        if (j + 2 * kT < j1) request(j + 2 * kT, id2, k_after, v_after);
+        const bool strange1 = more && !whole(j + kT, there1) && clear_values<KC>(w, v_next, j + kT, there1);
+        constexpr int kLast = S::kSteps - 1;
+        step<KC>(a, w, s, v_tile, kLast, k_next, 0, more, j + 32 * kLast, j + kT, strange,
+                 (uint32_t)(there >> 32 * kLast), (uint32_t)there1, lane);
+        there = there1;
+        strange = strange1;
+        id1 = id2;
+        id2 = id3;
+    };
+    for (int32_t j = j0; j < j1; j += 3 * kT) {
+        tile(j, k0, v0, k1, v1, k2, v2);
+        if (j + kT >= j1) break;
+        tile(j + kT, k1, v1, k2, v2, k0, v0);
+        if (j + 2 * kT >= j1) break;
+        tile(j + 2 * kT, k2, v2, k0, v0, k1, v1);
     }
 }
 
 template <int KC>
-__global__ __launch_bounds__(kThreads, KC <= 4 ? 2 : 1) void afx_attend_many_kernel(AttendArgs a) {
-    __shared__ __attribute__((aligned(16))) uint8_t k0[tile_bytes(KC)], k1[tile_bytes(KC)], v0[tile_bytes(KC)], v1[tile_bytes(KC)];
+__global__ __launch_bounds__(Shape<KC>::kThreads, KC <= 4 ? 2 : 1) void afx_attend_many_kernel(AttendArgs a) {
+    using S = Shape<KC>;
+    constexpr uint32_t kT = S::kT;
+    __shared__ __attribute__((aligned(16))) uint8_t k0[S::kBytes], k1[S::kBytes], k2[S::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t v0[S::kBytes], v1[S::kBytes], v2[S::kBytes];
     Tile t;
     const uint32_t u = blockIdx.x / a.kv_heads;
     t.kvh = blockIdx.x % a.kv_heads;  // (neighbouring workgroups, on different XCDs, read different heads)
     t.part = u % a.many_splits;
-    if (!find_tile(a, u / a.many_splits, t)) return;
+    if (!find_tile(a, u / a.many_splits, S::kRows, t)) return;
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, i = lane & 31, h = lane >> 5;
     const BatchRow &row = t.row;
-    const uint32_t wg_last = min(t.r0 + kManyRows, t.rows) - 1;
+    const uint32_t wg_last = min(t.r0 + S::kRows, t.rows) - 1;
     const uint32_t w0 = min(t.r0 + 32 * wave, wg_last), w1 = min(t.r0 + 32 * wave + 31, wg_last);
     Where w;
     w.table = a.table + (row.seq < a.n_seqs ? row.seq : 0) * a.table_stride;
@@ -296,8 +400,9 @@ __global__ __launch_bounds__(kThreads, KC <= 4 ? 2 : 1) void afx_attend_many_ker
     const int32_t j0 = base + (int32_t)((uint64_t)tiles * t.part / a.many_splits * kT);
     const int32_t j1 = base + (int32_t)((uint64_t)tiles * (t.part + 1) / a.many_splits * kT);
     // keys' dimensions behind the head's: zeros
-    for (uint32_t x = a.d / 8 * kT + threadIdx.x; x < 4 * KC * kT; x += kThreads)
-        *reinterpret_cast<u32x4 *>(k0 + x * 16) = *reinterpret_cast<u32x4 *>(k1 + x * 16) = u32x4{0, 0, 0, 0};
+    for (uint32_t x = a.d / 8 * kT + threadIdx.x; x < S::kBytes / 16; x += S::kThreads)
+        *reinterpret_cast<u32x4 *>(k0 + x * 16) = *reinterpret_cast<u32x4 *>(k1 + x * 16) =
+            *reinterpret_cast<u32x4 *>(k2 + x * 16) = u32x4{0, 0, 0, 0};
     Wave<KC> s;
     const uint32_t rr = min(t.r0 + 32 * wave + i, wg_last), tok = rr / a.group, head = t.kvh * a.group + rr % a.group;
     s.begin = row.begin(a, tok);
@@ -305,7 +410,7 @@ __global__ __launch_bounds__(kThreads, KC <= 4 ? 2 : 1) void afx_attend_many_ker
     const uint16_t *q = a.q + (row.from + tok) * a.q_stride + head * a.d;
 #pragma unroll
     for (int ks = 0; ks < 2 * KC; ++ks) s.q[ks] = load_q(a, q, 16 * ks + 8 * h);
-    run<KC>(a, w, s, k0, v0, k1, v1, j0, j1, wave, lane);
+    run<KC>(a, w, s, k0, v0, k1, v1, k2, v2, j0, j1, wave, lane);
     s.sum += __shfl_xor(s.sum, 32);
     if (t.r0 + 32 * wave + i > wg_last) return;
     const uint64_t at = row.from + tok;
@@ -347,7 +452,7 @@ int launch_attend_many(const AttendArgs &a, hipStream_t stream) {
     auto go = [&](auto kc) {
         constexpr int KC = decltype(kc)::value;
         return hipLaunchKernel(reinterpret_cast<const void *>(&afx_attend_many_kernel<KC>),
-                               dim3(a.kv_heads * a.many_tiles * a.many_splits), dim3(kThreads), p, 0,
+                               dim3(a.kv_heads * a.many_tiles * a.many_splits), dim3(Shape<KC>::kThreads), p, 0,
                                stream) == hipSuccess
                    ? AFX_OK
                    : AFX_E_HIP;
