@@ -184,12 +184,24 @@ Plan plan(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t
     if (many) {
         const uint64_t rows = 32 * many_waves((int)up(kv->head_dim, 32)), tiles = up((uint64_t)m * group, rows);
         s.many_tiles = (uint32_t)((uint64_t)m * group / rows + n_rows);
-        // whole rounds of one workgroup a CU, parts of 256 tokens at least
+        // Parts of 256 tokens at least, of the number that costs least by an estimate in us: a workgroup's token costs
+        // 0.022 of its round and 0.012 more as far as every CU has one, its start and end 12, a join 10 and 8 more per
+        // 81920 rows of a part. Measured, with 40 query and 8 key-value heads of 128 (tokens over tokens):
+        //   parts              1       2       3       4
+        //   2048 over 2048    88 us  125     130     153
+        //   2048 over 4096   205     232     236     249
+        //   2048 over 8192   454     436     422     426
+        //   2048 over 16384  927     809     768     754
+        //   512 over 8192    247     150     117     160
+        //   64 over 16384    475     248     173     134   (16: 59)
         const uint64_t most_splits = std::min<uint64_t>(16, std::max<uint64_t>(1, tokens / 256));
+        const double length = (double)tokens - (p->causal ? (double)std::min(most, tokens) / 2 : 0);
         double best = 1e30;
         for (uint64_t n = 1; n <= most_splits; ++n) {
-            const double cost = (double)up(tiles * kv->kv_heads * n, 256) / (double)n * (1 + 0.02 * (double)(n - 1));
-            if (cost < best * 0.98) best = cost, s.many_splits = (uint32_t)n;
+            const double units = (double)(tiles * kv->kv_heads * n) / 256, rounds = std::ceil(units);
+            const double join = n > 1 ? 10 + 8 * (double)n * (double)((uint64_t)m * p->q_heads) / 81920 : 0;
+            const double cost = length / (double)n * (0.022 * rounds + 0.012 * units) + 12 * rounds + join;
+            if (cost < best) best = cost, s.many_splits = (uint32_t)n;
         }
         if (s.many_splits > 1) s.many_sums = (uint64_t)m * p->q_heads * s.many_splits;
     }
