@@ -249,7 +249,7 @@ int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page
         return AFX_E_MISALIGNED;
     const Plan w = plan(p, kv, n_rows, m);
     const uint64_t need = w.bytes(kv->head_dim);
-    if ((uint64_t)kv->kv_heads * std::max((uint64_t)n_rows * std::max(w.few_rows, 1u),
+    if ((uint64_t)kv->kv_heads * std::max((uint64_t)n_rows * std::max(w.few_rows, w.few_splits),
                                           (uint64_t)w.many_tiles * w.many_splits) >= 1ull << 24)
         return AFX_E_UNSUPPORTED;
     if (need && !ws_dev) return AFX_E_INVALID_ARG;
