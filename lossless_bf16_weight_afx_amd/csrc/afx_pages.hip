@@ -8,7 +8,8 @@
 // same ids. Latency bounds it: one workgroup reads 16 KB of counts at a time
 // with the next 16 KB on their way. The bytes of pages that have to be copied
 // are moved by a second launch over all CUs, 16 bytes a lane and four loads in
-// flight; memory bounds that.
+// flight; memory bounds that (the live half of 80 planes moved to the front:
+// 154 us, 5.0 TB/s read and written; the plan before it 5).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
