@@ -22,7 +22,7 @@
 //
 // With 40 query and 8 key-value heads of 128: one token of each of 64
 // sequences of up to 8192 tokens takes 191 us, and 5 for the join (1.08 GB of
-// cache, 5.6 TB/s); one token over 131072 86 us with its join (537 MB, 6.2 TB/s).
+// cache, 5.6 TB/s); one token over 131072 81 us (537 MB, 6.6 TB/s), and 5.
 #include <type_traits>
 
 #include "afx_attend.h"
