@@ -191,6 +191,16 @@ def test_long_sequences_in_parts(length, new):
     b.check()
 
 
+@pytest.mark.parametrize("length", [900, 1000, 1500, 2000, 3000, 4000])
+@pytest.mark.parametrize("new, window", [(50, 0), (140, 0), (140, 700)])
+def test_any_number_of_parts(length, new, window):
+    """Numbers of parts that do not divide the tiles, rows that see nothing of some of them."""
+    b = Batch(length + new + window, [length, 260], [(0, new), (1, 40)], kv_heads=2, group=3, dim=64, page=32, spread=1.5)
+    b.upload()
+    b.run(scale=0.125, window=window)
+    b.check()
+
+
 @pytest.mark.parametrize("new", [1, 60])
 def test_scores_that_rise_and_fall(new):
     """Keys that grow along the sequence move the running maximum at every
