@@ -107,8 +107,9 @@ class Attention:
         step's new tokens, in this object's buffers (views of its first rows);
         their keys and values are in the cache's layer afterwards. pos: int32
         [n_axes, tokens], the tokens' positions, if they are not their places
-        in their sequences. r may not lie in this object's buffers, but for r'
-        of the last pass."""
+        in their sequences (each axis a row of its own in memory, also where
+        axes agree). r may not lie in this object's buffers, but for r' of the
+        last pass."""
         import torch
 
         m, c = r.shape[0], self.cache
@@ -123,15 +124,16 @@ class Attention:
         if pos is None and self.n_axes > 1:
             raise ValueError(f"positions along {self.n_axes} axes have to be told")
         if pos is not None and (pos.dtype != torch.int32 or pos.shape != (self.n_axes, m) or pos.stride(1) != 1
-                                or pos.device != c.device):
-            raise ValueError(f"positions are an int32 [{self.n_axes}, {m}] tensor on {c.device}, rows whole")
+                                or (self.n_axes > 1 and pos.stride(0) < m) or pos.device != c.device):
+            raise ValueError(f"positions are an int32 [{self.n_axes}, {m}] tensor on {c.device}, rows whole and each in "
+                             "memory of its own (not expanded)")
         r_ptr, ld = r.data_ptr(), r.stride(0) if m > 1 else self.d  # (one row's stride may be anything)
         if self._own(r_ptr, ld, m):
             raise ValueError("the residual stream lies in buffers that this object writes before it has read them")
         d, nq, nk, n = self.d, self.nq, self.nk, step.seqs.numel()
         y = self.y.data_ptr()
         q, k, v, b = y, y + 4 * m * nq, y + 4 * m * (nq + nk), y + 4 * m * (nq + 2 * nk)
-        pos_ptr, pos_ld = (step.pos.data_ptr(), m) if pos is None else (pos.data_ptr(), max(pos.stride(0), m))
+        pos_ptr, pos_ld = (step.pos if pos is None else pos).data_ptr(), pos.stride(0) if self.n_axes > 1 else m
         xn, xn_next = self.xn.data_ptr(), 0 if self.xn_next is None else self.xn_next.data_ptr()
         p = self._attend(m, step.max_new)
         if afx.afx_attend_workspace(p, self.kv, n, m) > self.ws.numel():
