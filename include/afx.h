@@ -535,7 +535,8 @@ int afx_attend_workspace(const afx_attend *p, const afx_kv_pages *kv, uint32_t n
  * every run. Enqueued on stream; returns without waiting. Errors:
  * AFX_E_INVALID_ARG (NULL pointer, a count out of its range, a table of other
  * pages, a stride shorter than its row, outputs sharing bytes with each other
- * or an input), AFX_E_UNSUPPORTED (the cache's sizes as above, m above 2^23,
+ * or an input), AFX_E_UNSUPPORTED (the cache's sizes as above, max_pages *
+ * page_tokens above 2^31 - 1024, m above 2^23,
  * n_rows above 2^16, a stride of 2^28 or more, more work than one launch
  * takes: kv_heads times the rows' parts or query rows, or times the tiles'
  * parts, of 2^24 or more), AFX_E_MISALIGNED (q, out or the workspace not

@@ -54,8 +54,9 @@ class PagedCache:
                              f"multiple of 8 up to {afx.MAX_HEAD_DIM}, and pages of 16, 32, 64, 128 or 256")
         if max_rows > afx.MAX_PAGE_ROWS or max_seqs > 1 << 20 or max_tokens > 1 << 23:
             raise ValueError(f"at most {afx.MAX_PAGE_ROWS} rows, 2^20 sequences and 2^23 tokens")
-        if n_pages * page_tokens >= 1 << 31 or max_pages * page_tokens >= 1 << 31 or 2 * layers > 65535:
-            raise ValueError("a pool, and a sequence, are of fewer than 2^31 tokens, and a cache of at most 32767 layers")
+        if n_pages * page_tokens >= 1 << 31 or max_pages * page_tokens > (1 << 31) - 1024 or 2 * layers > 65535:
+            raise ValueError("a pool is of fewer than 2^31 tokens, a sequence of up to 2^31 - 1024, and a cache of at most "
+                             "32767 layers")
         self.layers, self.kv_heads, self.head_dim = layers, kv_heads, head_dim
         self.n_pages, self.page_tokens, self.max_pages = n_pages, page_tokens, max_pages
         self.max_seqs, self.max_rows, self.max_tokens = max_seqs, max_rows, max_tokens

@@ -27,6 +27,9 @@ constexpr uint32_t kFewTokens = 32;    // tokens of a wave's tile in the kernel 
 // dimensions in units of 32: two on a SIMD while their registers allow it.
 constexpr uint32_t many_waves(int kc) { return kc <= 4 ? 8 : 4; }
 constexpr uint32_t kMaxSplits = 256;   // parts that a row's tokens are cut into
+// Tokens that a sequence may have: positions are int32, and both kernels look
+// up pages, and count, up to 512 positions behind a sequence's last.
+constexpr uint64_t kMaxPositions = (1ull << 31) - 1024;
 
 struct AttendArgs {
     const uint16_t *q, *k, *v;

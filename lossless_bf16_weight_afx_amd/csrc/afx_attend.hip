@@ -240,6 +240,7 @@ int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page
     if (rc == AFX_OK) rc = check_table(t, false);
     if (rc != AFX_OK) return rc;
     if (t->n_pages != kv->n_pages || t->page_tokens != kv->page_tokens) return AFX_E_INVALID_ARG;
+    if ((uint64_t)t->max_pages * t->page_tokens > kMaxPositions) return AFX_E_UNSUPPORTED;
     if (m == 0 || n_rows == 0) return AFX_OK;
     const uint64_t width = (uint64_t)p->q_heads * kv->head_dim;
     if (!starts_dev || !q_dev || !out_dev || q_stride < width || out_stride < width || (!seqs_dev && n_rows > t->n_seqs))
