@@ -536,10 +536,11 @@ int afx_attend_workspace(const afx_attend *p, const afx_kv_pages *kv, uint32_t n
  * AFX_E_INVALID_ARG (NULL pointer, a count out of its range, a table of other
  * pages, a stride shorter than its row, outputs sharing bytes with each other
  * or an input), AFX_E_UNSUPPORTED (the cache's sizes as above, max_pages *
- * page_tokens above 2^31 - 1024, m above 2^23,
- * n_rows above 2^16, a stride of 2^28 or more, more work than one launch
- * takes: kv_heads times the rows' parts or query rows, or times the tiles'
- * parts, of 2^24 or more), AFX_E_MISALIGNED (q, out or the workspace not
+ * page_tokens above 2^31 - 1024, m above 2^23, n_rows above 2^16, a stride
+ * of 2^28 or more, more work than one launch takes: kv_heads times the rows'
+ * parts or query rows of 2^24 or more, or kv_heads times the parts of all
+ * tiles of 256 query rows of 2^23 or more (above 128 dimensions: of 128 rows,
+ * 2^24)), AFX_E_MISALIGNED (q, out or the workspace not
  * 16-byte aligned, strides not multiples of 8, or lse, starts, seqs, len or
  * the table not 4-byte aligned), AFX_E_BUFFER_TOO_SMALL, AFX_E_HIP. */
 int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page_table *t, uint32_t n_rows,

@@ -250,8 +250,12 @@ int afx_attend_async(const afx_attend *p, const afx_kv_pages *kv, const afx_page
         return AFX_E_MISALIGNED;
     const Plan w = plan(p, kv, n_rows, m);
     const uint64_t need = w.bytes(kv->head_dim);
-    if ((uint64_t)kv->kv_heads * std::max((uint64_t)n_rows * std::max(w.few_rows, w.few_splits),
-                                          (uint64_t)w.many_tiles * w.many_splits) >= 1ull << 24)
+    // a launch takes fewer than 2^32 threads
+    const uint64_t few_blocks = (uint64_t)kv->kv_heads * n_rows * std::max(w.few_rows, w.few_splits);
+    const uint64_t many_blocks = (uint64_t)kv->kv_heads * w.many_tiles * w.many_splits;
+    const uint64_t joins = w.many_sums ? up((uint64_t)m * p->q_heads, kJoinThreads / (kv->head_dim / 4)) : 0;
+    if (std::max(few_blocks, joins) * kJoinThreads >= 1ull << 32 ||
+        many_blocks * 64 * many_waves((int)up(kv->head_dim, 32)) >= 1ull << 32)
         return AFX_E_UNSUPPORTED;
     if (need && !ws_dev) return AFX_E_INVALID_ARG;
     if (need && !aligned({ws_dev}, 16)) return AFX_E_MISALIGNED;
