@@ -156,7 +156,7 @@ Plan plan(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t
     Plan s{};
     const uint32_t group = p->q_heads / kv->kv_heads;
     const uint64_t most = std::max<uint64_t>(1, std::min(p->max_new, m));  // new tokens of a sequence
-    uint64_t tokens = std::max<uint64_t>(1, p->max_len);                   // that its queries see
+    uint64_t tokens = std::min(std::max<uint64_t>(1, p->max_len), kMaxPositions);  // that its queries see
     if (p->window) tokens = std::min<uint64_t>(tokens, (p->causal ? 0 : tokens) + p->window + most);
     const bool few = most * group <= 32, many = !few;
     s.few_rows = few ? (uint32_t)(most * group) : n_rows > 1 ? 32 : 0;
