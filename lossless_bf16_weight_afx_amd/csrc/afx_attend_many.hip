@@ -302,8 +302,8 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
             if constexpr (kT == 64) {
                 if (piece < chunks) load_to_lds(pk + piece * w.size * 8, k_tile + piece * 1024);
             } else {
-                const uint32_t chunk = 2 * piece + lane / 32;  // (a last one behind the head's is loaded twice)
-                if (2 * piece < chunks) load_to_lds(pk + min(chunk, chunks - 1) * w.size * 8, k_tile + piece * 1024);
+                const uint32_t chunk = 2 * piece + lane / 32;  // (behind the head's last one the zeros stay)
+                if (chunk < chunks) load_to_lds(pk + chunk * w.size * 8, k_tile + piece * 1024);
             }
         }
 #pragma unroll
