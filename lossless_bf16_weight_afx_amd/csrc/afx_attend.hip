@@ -10,6 +10,9 @@
 // workgroups to fill the card, tokens are cut into parts, whose sums (FP32) a
 // last launch joins: with M the largest of the parts' M_i,
 //   o = sum_i 2^(M_i - M) o_i / sum_i 2^(M_i - M) l_i.
+// A part whose factor has become 0 is added too: an infinity or NaN in it that
+// the query sees shows (0 times it is NaN), as it does beside the largest
+// score in one part.
 #include <algorithm>
 #include <cmath>
 
@@ -58,8 +61,7 @@ __global__ __launch_bounds__(kJoinThreads) void afx_attend_join_few_kernel(Atten
 #pragma unroll 4
         for (uint32_t i = team; i < n; i += teams) {
             const float w = weight[i];
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(a.few_o + (p + i) * a.d + 4 * quad);
-            if (w != 0.f) o += w * v;
+            o += w * *reinterpret_cast<const f32x4 *>(a.few_o + (p + i) * a.d + 4 * quad);
         }
     }
     sums[threadIdx.x] = o;
@@ -100,9 +102,10 @@ __device__ inline void join_row(const AttendArgs &a, const float *po, const floa
         o *= old;
 #pragma unroll
         for (uint32_t i = 0; i < kAtOnce; ++i) {
-            const float w = i0 + i < n && ml[i].x != -INFINITY ? exp2_fast(ml[i].x - base) : 0.f;
-            sum += w * ml[i].y;
-            if (w != 0.f) o += w * v[i];
+            const bool once = i0 + i < n;  // (behind the last part it is loaded again)
+            const float w = once && ml[i].x != -INFINITY ? exp2_fast(ml[i].x - base) : 0.f;
+            sum += w * (once ? ml[i].y : 0.f);
+            o += w * (once ? v[i] : f32x4{0.f, 0.f, 0.f, 0.f});
         }
     }
     const float k = sum == 0.f ? 0.f : 1.f / sum;

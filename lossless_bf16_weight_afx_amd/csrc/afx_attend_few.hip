@@ -340,7 +340,8 @@ __device__ __forceinline__ void unit(const AttendArgs &a, const Part &t, uint32_
                 const float2 ml = lds.ml[v][at];
                 const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
                 sum += f * ml.y;
-                if (f != 0.f) o += f * *reinterpret_cast<const f32x4 *>(&lds.o[v][at][4 * quad]);
+                // (also where f has become 0: an infinity or NaN that a row sees shows, wherever the tokens are cut)
+                o += f * *reinterpret_cast<const f32x4 *>(&lds.o[v][at][4 * quad]);
             }
             const uint32_t tok = row.from + rr / a.group, h = kvh * a.group + rr % a.group;
             if (t.splits == 1) {

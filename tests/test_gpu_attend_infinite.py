@@ -35,3 +35,29 @@ def test_scores_of_minus_infinity_from_any_dimension(dim, new):
     b.upload()
     b.run(scale=dim ** -0.5)
     b.check()
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("new, length, max_len", [(1, 300, 300), (1, 5000, 5000), (6, 5000, 5000), (1, 30000, 30000),
+                                                  (60, 300, 300), (60, 5000, 5000)])
+def test_what_a_query_sees_shows_however_the_work_is_cut(new, length, max_len, value):
+    """A value that is infinite or NaN at a score of 256 below the largest: its weight is above 0, so that the output is
+    no number that is finite, wherever its token stands beside the largest one."""
+    top = 37
+    for far in (38, 45, 70, 100, 200, length - new - 20):
+        b = Batch(far, [length], [(0, new)], kv_heads=1, group=2, dim=64)
+        b.q[:] = 0.0
+        b.q[:, [0, 64]] = 16.0
+        b.keys[0][:] = 0.0
+        b.keys[0][top, 0, 0] = 8.0
+        b.keys[0][far, 0, 0] = -8.0
+        b.values[0][far, 0, 3] = value
+        b.upload()
+        b.run(scale=1.0, max_len=max_len)
+        out = b.out[:new].reshape(new, 2, 64).cpu()
+        bad = out[:, :, 3]
+        assert bool((~torch.isfinite(bad)).all()), f"token {far}: {bad[0, 0]} where the value is {value}"
+        assert not math.isnan(value) or bool(torch.isnan(bad).all())
+        rest = [d for d in range(64) if d != 3]
+        # the others are the top token's (all other weights together: 30000 e^-128)
+        assert torch.equal(out[:, :, rest], b.values[0][top, 0, rest].expand(new, 2, 63))
