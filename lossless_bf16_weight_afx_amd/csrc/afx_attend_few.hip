@@ -16,8 +16,8 @@
 //
 // The next tile's keys are requested when this tile's scores are done with
 // them, its values after the second product: one of both is always on its
-// way. The running maximum moves only when a score exceeds it by 8 (a factor
-// 2^8): most tiles exchange nothing between lanes. Weights then lie in 0..2^8
+// way. A row's running maximum moves only when one of its scores exceeds it by
+// 8 (a factor 2^8): most tiles exchange nothing between lanes. Weights then lie in 0..2^8
 // and lose nothing, as their rounding to BF16 is relative.
 //
 // With 40 query and 8 key-value heads of 128: one token of each of 64
@@ -138,9 +138,10 @@ __device__ __forceinline__ void weights(const AttendArgs &a, Wave<KC, RG> &s, co
         if (__any(best > s.top[x] + kSlack)) {
             best = fmaxf(best, __shfl_xor(best, 16));
             best = fmaxf(best, __shfl_xor(best, 32));
-            const float now = fmaxf(s.top[x], best);
-            const float f = now == -INFINITY ? 1.f : exp2_fast(s.top[x] - now);
-            s.top[x] = now;
+            // (not with another row's: what this row does not see would change its bits)
+            const bool moves = best > s.top[x] + kSlack;
+            const float f = moves ? exp2_fast(s.top[x] - best) : 1.f;
+            s.top[x] = moves ? best : s.top[x];
             s.sum[x] *= f;
 #pragma unroll
             for (int t = 0; t < 2 * KC; ++t) s.o[x][t] *= f;

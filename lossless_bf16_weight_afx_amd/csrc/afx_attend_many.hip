@@ -20,8 +20,8 @@
 // and its largest score is found while they multiply the first step's values.
 // Its keys thus belong to the next tile at a tile's last step, where the
 // barrier stands; three tiles of LDS let the tile after that be requested
-// there, with a tile's time to arrive. The running maximum moves only when a
-// score exceeds it by 8 (a factor 2^8), as in afx_attend_few.hip.
+// there, with a tile's time to arrive. A row's running maximum moves only when
+// one of its scores exceeds it by 8 (a factor 2^8), as in afx_attend_few.hip.
 //
 // 2048 tokens over 16384, 40 query and 8 key-value heads of 128: 670-790 us
 // as the clock allows (0.83-0.96 PFLOP/s), and 33 for the join of 4 parts. Of
@@ -121,14 +121,15 @@ __device__ inline float largest(const f32x16 &s) {
     return best;
 }
 
-// Moves the running maximum to the scores of the next step, where one exceeds it by kSlack.
+// Moves the rows' running maxima to their scores of the next step, where one exceeds its row's by kSlack.
 template <int KC>
 __device__ __forceinline__ void follow(Wave<KC> &s, float best) {
     if (!__any(best > s.top + kSlack)) return;
     best = fmaxf(best, __shfl_xor(best, 32));
-    const float now = fmaxf(s.top, best);
-    const float f = now == -INFINITY ? 1.f : exp2_fast(s.top - now);
-    s.top = now;
+    // (not with another row's: what this row does not see would change its bits)
+    const bool moves = best > s.top + kSlack;
+    const float f = moves ? exp2_fast(s.top - best) : 1.f;
+    s.top = moves ? best : s.top;
     s.sum *= f;
 #pragma unroll
     for (int t = 0; t < KC; ++t) s.o[t] *= f;

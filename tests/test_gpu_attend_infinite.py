@@ -61,3 +61,30 @@ def test_what_a_query_sees_shows_however_the_work_is_cut(new, length, max_len, v
         rest = [d for d in range(64) if d != 3]
         # the others are the top token's (all other weights together: 30000 e^-128)
         assert torch.equal(out[:, :, rest], b.values[0][top, 0, rest].expand(new, 2, 63))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 136, 256])
+@pytest.mark.parametrize("length, new", [(200, 6), (4000, 6), (150, 70), (2000, 70)])
+@pytest.mark.parametrize("value", [1.0])
+@pytest.mark.parametrize("window", [0, 50])
+def test_what_a_query_does_not_see_changes_none_of_its_bits(dim, length, new, value, window):
+    """The last two new tokens' keys and values, and what only the first new token's window reaches, are replaced."""
+    b = Batch(dim + length + new, [length], [(0, new)], kv_heads=1, group=3, dim=dim)
+    b.upload()
+    how = dict(scale=dim ** -0.5, window=window)
+    b.run(**how)
+    b.check()
+    out, lse = b.out.clone(), b.lse.clone()
+    places = [length - 1, length - 2]
+    if window:
+        places.append(length - new - window + 1)  # (the first new token's first)
+    for at in places:
+        b.keys[0][at] = b.q[new - 1, :dim] * 4  # larger scores than any
+        b.values[0][at, 0, ::3] = value
+    b.upload()
+    b.run(**how)
+    first, end = 1 if window else 0, new - 2
+    assert torch.equal(b.lse[first:end], lse[first:end])
+    assert torch.equal(b.out[first:end].view(torch.int16), out[first:end].view(torch.int16))
+    changed = b.out[end:new].reshape(2, 3, dim)[:, :, ::3].float()
+    assert math.isfinite(value) == bool(torch.isfinite(changed).all())
