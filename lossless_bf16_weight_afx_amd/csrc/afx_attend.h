@@ -9,6 +9,13 @@
 // scale2 = |scale| log2(e); the scale's sign goes to q (a scale of 0 makes q 0
 // and scale2 1), so that the largest product is the largest score and minus
 // infinity stays what it is.
+//
+// Infinite and NaN values. In a tile of tokens that all rows see, the matrix
+// cores bring them to all rows. In one that some rows do not see, 0 times them
+// would be NaN: they are multiplied as 0, and added after the last tile to the
+// outputs of the rows that see them (as they are: a weight would not make them
+// finite). The other rows' sums are those of any finite value in their place,
+// bit for bit.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -105,6 +112,12 @@ __device__ inline uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t
 __device__ inline float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ inline uint32_t pack2(float lo, float hi) { return to_bf16(lo) | ((uint32_t)to_bf16(hi) << 16); }
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// Two BF16 values with infinities and NaN as zeros, and whether a value is one.
+__device__ inline uint32_t finite2(uint32_t v) {
+    const uint32_t odd = ((v & 0x7F807F80u) + 0x00800080u) >> 15 & 0x00010001u;  // (only all ones carry into bit 15)
+    return v & ~(odd * 0xFFFFu);
+}
+__device__ inline bool odd(uint16_t v) { return (v & 0x7F80u) == 0x7F80u; }
 // ln of the sum of e^score, from M and the sum of weights
 __device__ inline float lse_of(float top, float sum) {
     return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;

@@ -41,7 +41,6 @@ struct Wave {
     bf16x8 q[RG][KC];
     f32x4 o[RG][kDT];
     float top[RG], sum[RG];
-    int32_t begin[RG], end[RG];  // positions that the lane's row sees
 };
 
 struct Where {
@@ -50,6 +49,9 @@ struct Where {
     uint32_t page_elems, size, shift, d;
     int32_t lo, hi;      // positions that all rows see
     int32_t first, last; // and any
+    // In LDS: begin and end of what each of the wave's rows sees. (Only partial tiles need them; at 256 dimensions the
+    // hot loop has no registers left.)
+    int2 *range;
 };
 
 // 8 tokens' worth of a value fragment without the tokens that ok leaves out.
@@ -58,14 +60,6 @@ __device__ inline u32x4 only(u32x4 v, uint32_t ok) {
     for (int i = 0; i < 4; ++i)
         v[i] &= ((ok >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((ok >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
     return v;
-}
-
-// Whether one of 8 values is an infinity or NaN.
-__device__ inline bool odd(u32x4 v) {
-    uint32_t t = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t |= (v[i] & 0x7F807F80u) + 0x00800080u;  // (only all ones carry into bit 15)
-    return t & 0x80008000u;
 }
 
 __device__ inline u32x4 once(const uint16_t *p) {  // (read by this wave only)
@@ -164,9 +158,11 @@ __device__ __forceinline__ void add_values(Wave<KC, RG> &s, const u32x4 (&vf)[2 
             s.o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf[t]), p[x], s.o[x][t], 0, 0, 0);
 }
 
-// The tile at j, of which some rows see only a part, or not all pages are in the cache.
+// The tile at j, of which some rows see only a part, or not all pages are in
+// the cache. Returns whether there are infinities or NaN among its values
+// that some row sees, which have been left out.
 template <int KC, int RG, bool kFull>
-__device__ __forceinline__ void partial_tile(const AttendArgs &a, const Where &w, Wave<KC, RG> &s, int32_t j,
+__device__ __forceinline__ bool partial_tile(const AttendArgs &a, const Where &w, Wave<KC, RG> &s, int32_t j,
                                              uint32_t lane) {
     lane = opaque(lane);
     const uint32_t c = lane & 15, g = lane >> 4;
@@ -178,6 +174,9 @@ __device__ __forceinline__ void partial_tile(const AttendArgs &a, const Where &w
     f32x4 sc[RG][2];
     scores<KC, RG, kFull>(w, s, kf, g, sc);
     uint32_t any = 0;  // of the lane's 8 tokens, those that some row sees
+    int2 see[RG];
+#pragma unroll
+    for (int x = 0; x < RG; ++x) see[x] = w.range[16 * x + c];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int32_t at = j + 8 * (int32_t)g + e;
@@ -185,50 +184,57 @@ __device__ __forceinline__ void partial_tile(const AttendArgs &a, const Where &w
         any |= there && at >= w.first && at < w.last ? 1u << e : 0u;
 #pragma unroll
         for (int x = 0; x < RG; ++x)
-            if (!there || at < s.begin[x] || at >= s.end[x]) sc[x][e / 4][e % 4] = -INFINITY;
+            if (!there || at < see[x].x || at >= see[x].y) sc[x][e / 4][e % 4] = -INFINITY;
     }
     bf16x8 p[RG];
     weights<KC, RG>(a, s, sc, p);
-    bool strange = false;
+    uint32_t strange = 0;
 #pragma unroll
     for (int t = 0; t < 2 * KC; ++t) {
         vf[t] = only(vf[t], any);
-        strange |= odd(vf[t]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = finite2(vf[t][i]);
+            strange |= v ^ vf[t][i];
+            vf[t][i] = v;
+        }
     }
-    // (a strange one: value by value, so that it reaches only the rows that see it)
-    const int32_t odd_end = __any(strange) ? (int32_t)kFewTokens : 0;
-    if (odd_end == 0) add_values<KC, RG>(s, vf, p);
+    add_values<KC, RG>(s, vf, p);
+    return __any(strange != 0);
+}
+
+// The last place of a whole tile before j1.
+__device__ inline int32_t whole_end(const Where &w, int32_t j1) { return min(w.hi - (int32_t)kFewTokens, j1 - 1); }
+
+// The infinities and NaN that partial_tile left out of the wave's tiles from
+// j0 to j1 are added to the outputs of a row that sees begin .. end - 1, if it
+// sees them: to the lane's four of every 16, row[dim].
+__device__ __forceinline__ void add_strange(const AttendArgs &a, const Where &w, int32_t begin, int32_t end, int32_t j0,
+                                            int32_t j1, uint32_t g, float *row) {
+    auto page = [&](int32_t at) { return (uint32_t)w.table[min((uint32_t)at >> w.shift, a.max_pages - 1)]; };
 #pragma unroll 1
-    for (int e = 0; e < odd_end; ++e) {
-        const int32_t at = j + e;
-        const uint32_t page = __shfl(id, 16 * (e / 8));
-        if (page >= a.n_pages) continue;
-        const uint32_t own = opaque(4 * g);
-        const uint16_t *pv = w.v + (uint64_t)page * w.page_elems + (at & (w.size - 1) & ~7u) * w.d + at % 8 + own * 8;
+    for (int32_t j = j0; j < j1; j += (int32_t)(kWaves * kFewTokens)) {
+        if (j >= w.lo && j <= whole_end(w, j1) && page(j) < a.n_pages && page(j + 16) < a.n_pages) continue;
+#pragma unroll 1
+        for (int32_t at = j; at < j + (int32_t)kFewTokens; ++at) {
+            const uint32_t id = page(at);
+            if (id >= a.n_pages || at < begin || at >= end) continue;
+            const uint16_t *v = w.v + (uint64_t)id * w.page_elems + ((uint32_t)at & (w.size - 1) & ~7u) * w.d + at % 8;
+#pragma unroll 1
+            for (uint32_t dim = 4 * g; dim < w.d; dim += 16)
 #pragma unroll
-        for (int x = 0; x < RG; ++x) {
-            const u32x4 bits = __builtin_bit_cast(u32x4, p[x]);
-            const uint32_t two = e / 2 % 4 == 0 ? bits[0] : e / 2 % 4 == 1 ? bits[1] : e / 2 % 4 == 2 ? bits[2] : bits[3];
-            const uint32_t got = __shfl(two, c + 16 * (e / 8));
-            const bool seen = at >= s.begin[x] && at < s.end[x];
-            const float weight = from_bf16((uint16_t)(e % 2 ? got >> 16 : got));
-#pragma unroll
-            for (int t = 0; t < 2 * KC; ++t) {
-                float v[4] = {};
-                if (kFull || 16 * t + own < w.d) {  // (d is a multiple of 8: all four or none)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = from_bf16(pv[(16 * t + r) * 8]);
+                for (uint32_t x = 0; x < 4; ++x) {
+                    const uint16_t value = v[(dim + x) * 8];
+                    if (odd(value)) row[dim + x] += from_bf16(value);
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) s.o[x][t][r] = seen ? s.o[x][t][r] + weight * v[r] : s.o[x][t][r];
-            }
         }
     }
 }
 
-// One pass over the wave's tiles from j0 to j1.
+// One pass over the wave's tiles from j0 to j1; whether partial_tile left out
+// values of one.
 template <int KC, int RG, bool kFull>
-__device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC, RG> &s, int32_t j0, int32_t j1,
+__device__ __forceinline__ bool run(const AttendArgs &a, const Where &w, Wave<KC, RG> &s, int32_t j0, int32_t j1,
                                     uint32_t wave, uint32_t lane) {
 #pragma unroll
     for (int x = 0; x < RG; ++x) {
@@ -241,7 +247,8 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
     const uint32_t g = lane >> 4;
     const Reads<KC, kFull> reads{a, w, lane & 15, g};
     int32_t j = j0 + (int32_t)(wave * kFewTokens);
-    const int32_t end = min(w.hi - (int32_t)kFewTokens, j1 - 1);  // the last place of a whole tile
+    const int32_t end = whole_end(w, j1);
+    bool strange = false;
     while (j < j1) {
         if (j >= w.lo && j <= end) {
             uint32_t id = reads.v_page(j), kid2 = reads.k_page(j + kStep), vid2 = reads.v_page(j + kStep);
@@ -266,15 +273,17 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
             }
             if (j > end) continue;
         }
-        if (j < j1) partial_tile<KC, RG, kFull>(a, w, s, j, lane);
+        if (j < j1) strange |= partial_tile<KC, RG, kFull>(a, w, s, j, lane);
         j += kStep;
     }
+    return strange;
 }
 
 template <int KC>
 struct Lds {
     float o[kWaves][16][32 * KC + 4];
     float2 ml[kWaves][16];
+    int2 range[kWaves][32];
 };
 
 // What a workgroup works on: a key-value head of batch row r, or one part of
@@ -292,7 +301,8 @@ __device__ __forceinline__ void unit(const AttendArgs &a, const Part &t, uint32_
     const BatchRow &row = t.row;
     const int32_t j0 = t.j0, j1 = t.j1;
     const uint32_t r = t.r, kvh = t.kvh, part = t.part;
-    const uint32_t tid = opaque(threadIdx.x), lane = tid % 64, wave = tid / 64, c = lane & 15, g = lane >> 4;
+    const uint32_t lane = opaque(threadIdx.x) % 64, c = lane & 15, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);  // (a scalar: so are the places of its tiles)
     const uint32_t rows = row.n * a.group;
     Where w;
     w.table = a.table + (row.seq < a.n_seqs ? row.seq : 0) * a.table_stride;
@@ -307,26 +317,31 @@ __device__ __forceinline__ void unit(const AttendArgs &a, const Part &t, uint32_
     w.last = row.end(a, last / a.group);
     w.lo = row.begin(a, last / a.group);
     w.hi = row.end(a, r0 / a.group);
+    w.range = lds.range[wave];
     Wave<KC, RG> s;
 #pragma unroll
     for (int x = 0; x < RG; ++x) {
         const uint32_t rr = min(r0 + 16 * x + c, last), t = rr / a.group;
-        s.begin[x] = row.begin(a, t);
-        s.end[x] = row.end(a, t);
+        w.range[16 * x + c] = make_int2(row.begin(a, t), row.end(a, t));  // (read by this wave)
         const uint16_t *q = a.q + (row.from + t) * a.q_stride + (kvh * a.group + rr % a.group) * a.d;
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc) s.q[x][kc] = load_q(a, q, 32 * kc + 8 * g);
     }
-    run<KC, RG, kFull>(a, w, s, j0, j1, wave, lane);
+    const bool strange = run<KC, RG, kFull>(a, w, s, j0, j1, wave, lane);
     // the waves' sums, 16 rows at a time
 #pragma unroll
     for (int x = 0; x < RG; ++x) {
+        const uint32_t tid = opaque(threadIdx.x), c = tid & 15, g = tid % 64 >> 4;  // (formed again: run has no room)
         s.sum[x] += __shfl_xor(s.sum[x], 16);
         s.sum[x] += __shfl_xor(s.sum[x], 32);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < kDT; ++t) *reinterpret_cast<f32x4 *>(&lds.o[wave][c][16 * t + 4 * g]) = s.o[x][t];
         if (g == 0) lds.ml[wave][c] = make_float2(s.top[x], s.sum[x]);
+        if (strange) {
+            const int2 see = lds.range[wave][16 * x + c];
+            add_strange(a, w, see.x, see.y, j0 + (int32_t)(wave * kFewTokens), j1, g, lds.o[wave][c]);
+        }
         __syncthreads();
         const uint32_t quads = a.d / 4;
         for (uint32_t i = tid; i < 16 * quads; i += kThreads) {

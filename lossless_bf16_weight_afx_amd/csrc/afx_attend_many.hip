@@ -151,12 +151,13 @@ __device__ __forceinline__ void hide(Wave<KC> &s, int32_t j, uint32_t there, uin
     }
 }
 
-// Values of the tile at j that no row of the workgroup sees become 0; whether
-// the others hold an infinity or NaN. there: which tokens have pages.
+// Values of the tile at j that no row of the workgroup sees become 0, and so
+// do infinities and NaN; whether there were such (in a scalar register: as a
+// lane's flag it costs the loop 60 registers). there: which tokens have pages.
 template <int KC>
-__device__ __forceinline__ bool clear_values(const Where &w, uint8_t *v_tile, int32_t j, uint64_t there) {
+__device__ __forceinline__ uint32_t clear_values(const Where &w, uint8_t *v_tile, int32_t j, uint64_t there) {
     using S = Shape<KC>;
-    uint32_t odd = 0;
+    uint32_t strange = 0;
     for (uint32_t x = opaque(threadIdx.x); x < S::kBytes / 16; x += S::kThreads) {
         u32x4 *p = reinterpret_cast<u32x4 *>(v_tile + x * 16);
         u32x4 v = *p;
@@ -167,38 +168,41 @@ __device__ __forceinline__ bool clear_values(const Where &w, uint8_t *v_tile, in
                 const int32_t at = j + (int32_t)t;
                 return (there >> t & 1) && at >= w.wg_first && at < w.wg_last;
             };
-            v[e] &= (seen(t8 + 2 * e) ? 0xFFFFu : 0u) | (seen(t8 + 2 * e + 1) ? 0xFFFF0000u : 0u);
-            odd |= (v[e] & 0x7F807F80u) + 0x00800080u;  // (only all ones carry into bit 15)
+            const uint32_t u = v[e] & ((seen(t8 + 2 * e) ? 0xFFFFu : 0u) | (seen(t8 + 2 * e + 1) ? 0xFFFF0000u : 0u));
+            v[e] = finite2(u);
+            strange |= u ^ v[e];
         }
         *p = v;
     }
-    return __syncthreads_or((odd & 0x80008000u) != 0);
+    return (uint32_t)__builtin_amdgcn_readfirstlane(__syncthreads_or(strange != 0));
 }
 
-// A step's values one by one, so that an infinity or NaN reaches only the
-// rows that see it.
-template <int KC>
-__device__ __forceinline__ void add_strange(Wave<KC> &s, bf16x8 p0, bf16x8 p1, const uint8_t *v_step, int32_t j,
-                                            uint32_t there, uint32_t lane) {
-    const uint32_t i = opaque(lane) & 31, own = opaque(lane) >> 5 << 2;
-    const u32x4 b0 = __builtin_bit_cast(u32x4, p0), b1 = __builtin_bit_cast(u32x4, p1);
+// The infinities and NaN that clear_values took out of the tiles from j0 to j1
+// are added to the row's outputs in memory, if it sees them: to those of the
+// lane, put(dim, value).
+template <int KC, class F>
+__device__ __forceinline__ void add_strange(const AttendArgs &a, const Where &w, const Wave<KC> &s, int32_t j0,
+                                            int32_t j1, uint32_t h, F put) {
+    constexpr int32_t kT = Shape<KC>::kT;
+    auto page = [&](int32_t at) { return (uint32_t)w.table[min((uint32_t)at >> a.page_shift, a.max_pages - 1)]; };
 #pragma unroll 1
-    for (uint32_t t = 0; t < 32; ++t) {
-        const uint32_t x = t / 2 % 4;
-        const uint32_t two = t < 16 ? x == 0 ? b0[0] : x == 1 ? b0[1] : x == 2 ? b0[2] : b0[3]
-                                    : x == 0 ? b1[0] : x == 1 ? b1[1] : x == 2 ? b1[2] : b1[3];
-        const uint32_t got = __shfl(two, i + 32 * (t / 8 % 2));
-        const float weight = from_bf16((uint16_t)(t % 2 ? got >> 16 : got));
-        const int32_t at = j + (int32_t)t;
-        const bool seen = (there >> t & 1) && at >= s.begin && at < s.end;
-        const uint16_t *values = reinterpret_cast<const uint16_t *>(v_step) + (t / 8 * 32 * KC + own) * 8 + t % 8;
+    for (int32_t j = j0; j < j1; j += kT) {
+        bool cleared = j < w.wg_lo || j + kT > w.wg_hi;
+        for (int32_t t = 0; t < kT; t += 16) cleared |= page(j + t) >= a.n_pages;
+        if (!cleared) continue;
+#pragma unroll 1
+        for (int32_t at = j; at < j + kT; ++at) {
+            const uint32_t id = page(at);
+            if (id >= a.n_pages || at < s.begin || at >= s.end) continue;
+            const uint16_t *v = w.v + (uint64_t)id * w.page_elems + ((uint32_t)at & (w.size - 1) & ~7u) * a.d + at % 8;
+#pragma unroll 1
+            for (uint32_t dim = 4 * h; dim < a.d; dim += 8)
 #pragma unroll
-        for (int d = 0; d < KC; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float v = from_bf16(values[(32 * d + (e & 3) + 8 * (e >> 2)) * 8]);
-                s.o[d][e] = seen ? s.o[d][e] + weight * v : s.o[d][e];
-            }
+                for (uint32_t x = 0; x < 4; ++x) {
+                    const uint16_t value = v[(dim + x) * 8];
+                    if (odd(value)) put(dim + x, from_bf16(value));
+                }
+        }
     }
 }
 
@@ -222,8 +226,8 @@ __device__ __forceinline__ void multiply_keys(Wave<KC> &s, const uint8_t *k_tile
 // the step's values, and the scores of the next step (step m of `next`).
 template <int KC>
 __device__ __forceinline__ void step(const AttendArgs &a, const Where &w, Wave<KC> &s, const uint8_t *v_tile, int n,
-                                     const uint8_t *next, int m, bool more, int32_t j, int32_t j_next, bool strange,
-                                     uint32_t there, uint32_t there_next, uint32_t lane) {
+                                     const uint8_t *next, int m, bool more, int32_t j_next, uint32_t there_next,
+                                     uint32_t lane) {
     using S = Shape<KC>;
     const uint32_t i = lane & 31, h = lane >> 5;
     const float base = s.top == -INFINITY ? 0.f : s.top;
@@ -238,28 +242,20 @@ __device__ __forceinline__ void step(const AttendArgs &a, const Where &w, Wave<K
         }
         s.sum += (part[0] + part[1]) + (part[2] + part[3]);
     };
-    float best;
-    if (!strange) {
-        const f32x16 was = s.sc;
-        const uint8_t *v_base = v_tile + ((4 * n + h) * S::kDims + i) * 16;
-        bf16x8 v[2 * KC];
-        // the next step's keys beside this one's weights
-        multiply_keys<KC>(s, next, m, lane);
-        weigh(was);
+    const f32x16 was = s.sc;
+    const uint8_t *v_base = v_tile + ((4 * n + h) * S::kDims + i) * 16;
+    bf16x8 v[2 * KC];
+    // the next step's keys beside this one's weights
+    multiply_keys<KC>(s, next, m, lane);
+    weigh(was);
 #pragma unroll
-        for (int x = 0; x < 2 * KC; ++x)
-            v[x] = *reinterpret_cast<const bf16x8 *>(v_base + (x / KC * 2 * S::kDims + 32 * (x % KC)) * 16);
-        // and its largest score beside this one's values
+    for (int x = 0; x < 2 * KC; ++x)
+        v[x] = *reinterpret_cast<const bf16x8 *>(v_base + (x / KC * 2 * S::kDims + 32 * (x % KC)) * 16);
+    // and its largest score beside this one's values
 #pragma unroll
-        for (int x = 0; x < 2 * KC; ++x)
-            s.o[x % KC] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[x], p[x / KC], s.o[x % KC], 0, 0, 0);
-        best = largest(s.sc);
-    } else {
-        weigh(s.sc);
-        add_strange<KC>(s, p[0], p[1], v_tile + 4 * n * S::kDims * 16, j, there, lane);
-        multiply_keys<KC>(s, next, m, opaque(lane));
-        best = largest(s.sc);
-    }
+    for (int x = 0; x < 2 * KC; ++x)
+        s.o[x % KC] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[x], p[x / KC], s.o[x % KC], 0, 0, 0);
+    float best = largest(s.sc);
     if (there_next != ~0u || j_next < w.lo || j_next + 32 > w.hi) {
         hide<KC>(s, j_next, there_next, lane);
         best = largest(s.sc);
@@ -267,10 +263,11 @@ __device__ __forceinline__ void step(const AttendArgs &a, const Where &w, Wave<K
     follow<KC>(s, more ? best * a.scale2 : -INFINITY);
 }
 
-// All tiles from j0 to j1. The buffers are objects of their own: of one array
-// the compiler would have every read wait for all loads into it.
+// All tiles from j0 to j1; whether clear_values took infinities or NaN out of
+// one. The buffers are objects of their own: of one array the compiler would
+// have every read wait for all loads into it.
 template <int KC>
-__device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC> &s, uint8_t *k0, uint8_t *v0,
+__device__ __forceinline__ uint32_t run(const AttendArgs &a, const Where &w, Wave<KC> &s, uint8_t *k0, uint8_t *v0,
                                     uint8_t *k1, uint8_t *v1, uint8_t *k2, uint8_t *v2, int32_t j0, int32_t j1,
                                     uint32_t wave, uint32_t lane) {
     using S = Shape<KC>;
@@ -282,7 +279,7 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
     for (int t = 0; t < KC; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s.o[t][e] = 0.f;
-    if (j0 >= j1) return;
+    if (j0 >= j1) return 0;
     auto page_of = [&](int32_t at) __attribute__((always_inline)) {  // of the lane's token of the tile at `at`
         return (uint32_t)w.table[min(((uint32_t)at + lane % kT) >> a.page_shift, a.max_pages - 1)];
     };
@@ -336,7 +333,7 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     __syncthreads();
     uint64_t there = tokens_there(id);
-    bool strange = false;
+    uint32_t strange = 0;
     if (!whole(j0, there)) strange = clear_values<KC>(w, v0, j0, there);
     multiply_keys<KC>(s, k0, 0, lane);
     if ((uint32_t)there != ~0u || j0 < w.lo || j0 + 32 > w.hi) hide<KC>(s, j0, (uint32_t)there, lane);
@@ -345,8 +342,8 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
                     uint8_t *v_after) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n + 1 < S::kSteps; ++n)
-            step<KC>(a, w, s, v_tile, n, k_tile, n + 1, true, j + 32 * n, j + 32 * (n + 1), strange,
-                     (uint32_t)(there >> 32 * n), (uint32_t)(there >> 32 * (n + 1)), lane);
+            step<KC>(a, w, s, v_tile, n, k_tile, n + 1, true, j + 32 * (n + 1),
+                     (uint32_t)(there >> 32 * (n + 1)), lane);
         // The last step multiplies the next tile's keys: it has to have arrived, in every wave. No wave is still in the
         // tile before this one, whose buffers take the tile after the next.
         const bool more = j + kT < j1;
@@ -355,12 +352,10 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
         const uint64_t there1 = tokens_there(id1);
         const uint32_t id3 = page_of(j + 3 * kT);
         if (j + 2 * kT < j1) request(j + 2 * kT, id2, k_after, v_after);
-        const bool strange1 = more && !whole(j + kT, there1) && clear_values<KC>(w, v_next, j + kT, there1);
+        if (more && !whole(j + kT, there1)) strange |= clear_values<KC>(w, v_next, j + kT, there1);
         constexpr int kLast = S::kSteps - 1;
-        step<KC>(a, w, s, v_tile, kLast, k_next, 0, more, j + 32 * kLast, j + kT, strange,
-                 (uint32_t)(there >> 32 * kLast), (uint32_t)there1, lane);
+        step<KC>(a, w, s, v_tile, kLast, k_next, 0, more, j + kT, (uint32_t)there1, lane);
         there = there1;
-        strange = strange1;
         id1 = id2;
         id2 = id3;
     };
@@ -371,6 +366,7 @@ __device__ __forceinline__ void run(const AttendArgs &a, const Where &w, Wave<KC
         if (j + 2 * kT >= j1) break;
         tile(j + 2 * kT, k2, v2, k0, v0, k1, v1);
     }
+    return strange;
 }
 
 template <int KC>
@@ -418,7 +414,7 @@ __global__ __launch_bounds__(Shape<KC>::kThreads, KC <= 4 ? 2 : 1) void afx_atte
     const uint16_t *q = a.q + (row.from + tok) * a.q_stride + head * a.d;
 #pragma unroll
     for (int ks = 0; ks < 2 * KC; ++ks) s.q[ks] = load_q(a, q, 16 * ks + 8 * h);
-    run<KC>(a, w, s, k0, v0, k1, v1, k2, v2, j0, j1, wave, lane);
+    const uint32_t strange = run<KC>(a, w, s, k0, v0, k1, v1, k2, v2, j0, j1, wave, lane);
     s.sum += __shfl_xor(s.sum, 32);
     if (t.r0 + 32 * wave + i > wg_last) return;
     const uint64_t at = row.from + tok;
@@ -437,6 +433,8 @@ __global__ __launch_bounds__(Shape<KC>::kThreads, KC <= 4 ? 2 : 1) void afx_atte
                 *reinterpret_cast<uint2 *>(out + dim) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
             }
         if (a.lse && h == 0) a.lse[at * a.q_heads + head] = lse_of(s.top, s.sum);
+        if (strange && s.sum != 0.f)
+            add_strange<KC>(a, w, s, j0, j1, h, [&](uint32_t dim, float v) { out[dim] = to_bf16(from_bf16(out[dim]) + v); });
     } else {
         const uint64_t p = (at * a.q_heads + head) * a.many_splits + t.part;
 #pragma unroll
@@ -449,6 +447,7 @@ __global__ __launch_bounds__(Shape<KC>::kThreads, KC <= 4 ? 2 : 1) void afx_atte
                     f32x4{s.o[d][e], s.o[d][e + 1], s.o[d][e + 2], s.o[d][e + 3]};
             }
         if (h == 0) a.many_ml[p] = make_float2(s.top, s.sum);
+        if (strange) add_strange<KC>(a, w, s, j0, j1, h, [&](uint32_t dim, float v) { a.many_o[p * a.d + dim] += v; });
     }
 }
 

@@ -65,7 +65,7 @@ def test_what_a_query_sees_shows_however_the_work_is_cut(new, length, max_len, v
 
 @pytest.mark.parametrize("dim", [64, 128, 136, 256])
 @pytest.mark.parametrize("length, new", [(200, 6), (4000, 6), (150, 70), (2000, 70)])
-@pytest.mark.parametrize("value", [1.0])
+@pytest.mark.parametrize("value", [1.0, math.nan, math.inf])
 @pytest.mark.parametrize("window", [0, 50])
 def test_what_a_query_does_not_see_changes_none_of_its_bits(dim, length, new, value, window):
     """The last two new tokens' keys and values, and what only the first new token's window reaches, are replaced."""
@@ -88,3 +88,19 @@ def test_what_a_query_does_not_see_changes_none_of_its_bits(dim, length, new, va
     assert torch.equal(b.out[first:end].view(torch.int16), out[first:end].view(torch.int16))
     changed = b.out[end:new].reshape(2, 3, dim)[:, :, ::3].float()
     assert math.isfinite(value) == bool(torch.isfinite(changed).all())
+
+
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("new, length", [(1, 700), (5, 700), (80, 700), (80, 3000)])
+def test_beside_pages_outside_the_cache(page, new, length):
+    """Tiles that every query sees but for a page that is not there."""
+    b = Batch(page + new, [length, 40], [(0, new), (1, 1)], kv_heads=2, group=3, dim=72, page=page)
+    for i in (1, 3):
+        b.table[0, i] = -1
+        b.there[0][page * i:page * (i + 1)] = False
+    for at, value in ((page - 1, math.inf), (2 * page, math.nan), (2 * page + 3, -math.inf), (4 * page, math.inf),
+                      (length - 1, math.nan), (length - new, math.inf)):
+        b.values[0][at, at % 2, at % 72] = value
+    b.upload()
+    b.run(scale=0.125)
+    b.check()
