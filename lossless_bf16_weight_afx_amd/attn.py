@@ -96,9 +96,12 @@ class Attention:
                 yield afx.afx_attend_workspace(self._attend(m, m), self.kv, n, m)
 
     def _own(self, ptr: int, ld: int, m: int) -> bool:
-        """Whether rows of a stream lie in buffers that the pass writes before it has read them: all but r'."""
+        """Whether rows of a stream lie in buffers that the pass writes before it has read them: all but r', which is
+        written row by row in the places of its own rows."""
         end = ptr + 2 * ((m - 1) * ld + self.d)
         own = [self.xn, self.qn, self.a, self.xn_next, self.y, self.ws, self.cache.data]
+        if ptr != self.r_out.data_ptr() or ld != self.d:
+            own.append(self.r_out[:m])
         return any(t is not None and ptr < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < end
                    for t in own)
 
@@ -109,7 +112,7 @@ class Attention:
         [n_axes, tokens], the tokens' positions, if they are not their places
         in their sequences (each axis a row of its own in memory, also where
         axes agree). r may not lie in this object's buffers, but for r' of the
-        last pass."""
+        last pass, from its first row on (or rows behind the new tokens')."""
         import torch
 
         m, c = r.shape[0], self.cache
