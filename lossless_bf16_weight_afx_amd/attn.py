@@ -80,20 +80,20 @@ class Attention:
         self.y = torch.empty(max_tokens * (nq + 2 * nk + d), dtype=torch.float32, device=dev)
         self.ws = torch.empty(max(max(self._workspaces()), 16), dtype=torch.uint8, device=dev)
 
-    def _attend(self, m: int, max_new: int, max_len: int | None = None) -> afx.afx_attend:
-        whole = self.cache.max_pages * self.cache.page_tokens
-        return afx.attend(self.q_heads, self.softmax_scale, True, self.window, max_new, whole if max_len is None else max_len)
+    def _attend(self, max_new: int, max_len: int) -> afx.afx_attend:
+        return afx.attend(self.q_heads, self.softmax_scale, True, self.window, max_new, max_len)
 
     def _workspaces(self):
-        """The workspaces of single tokens and of drafts of some tokens for every number of rows, and of prompts."""
-        rows = min(self.cache.max_rows, self.max_tokens)
-        for n in range(1, rows + 1):
-            for new in {1, 2, 4, 8}:
-                if n * new <= self.max_tokens:
-                    yield afx.afx_attend_workspace(self._attend(n * new, new), self.kv, n, n * new)
-        for m in {*range(16, self.max_tokens + 1, 16), self.max_tokens}:
-            for n in {1, min(4, rows), min(64, rows), rows}:
-                yield afx.afx_attend_workspace(self._attend(m, m), self.kv, n, m)
+        """The workspaces of single tokens and of drafts of some tokens for every number of rows, and of prompts, over
+        sequences of the cache's most tokens and of shorter ones (which may be cut into more parts)."""
+        rows, whole = min(self.cache.max_rows, self.max_tokens), self.cache.max_pages * self.cache.page_tokens
+        sizes = [(new, n, n * new) for n in range(1, rows + 1) for new in (1, 2, 4, 8) if n * new <= self.max_tokens]
+        sizes += [(m, n, m) for m in {*range(16, self.max_tokens + 1, 16), self.max_tokens}
+                  for n in {1, min(4, rows), min(64, rows), rows}]
+        lens = [256 << i for i in range(whole.bit_length()) if 256 << i < whole] + [whole]
+        for new, n, m in sizes:
+            for length in lens:
+                yield afx.afx_attend_workspace(self._attend(new, length), self.kv, n, m)
 
     def _own(self, ptr: int, ld: int, m: int) -> bool:
         """Whether rows of a stream lie in buffers that the pass writes before it has read them: all but r', which is
@@ -138,9 +138,9 @@ class Attention:
         q, k, v, b = y, y + 4 * m * nq, y + 4 * m * (nq + nk), y + 4 * m * (nq + 2 * nk)
         pos_ptr, pos_ld = (step.pos if pos is None else pos).data_ptr(), pos.stride(0) if self.n_axes > 1 else m
         xn, xn_next = self.xn.data_ptr(), 0 if self.xn_next is None else self.xn_next.data_ptr()
-        p = self._attend(m, step.max_new)
+        p = self._attend(step.max_new, step.max_len)
         if afx.afx_attend_workspace(p, self.kv, n, m) > self.ws.numel():
-            p = self._attend(m, step.max_new, 1)  # (a step of unusual sizes: in one part, which needs none)
+            p = self._attend(step.max_new, 1)  # (a step of unusual sizes: in one part, which needs none)
         s = torch.cuda.current_stream(c.device).cuda_stream
         with torch.cuda.device(c.device):
             self.y[:m * (nq + 2 * nk + d)].zero_()

@@ -21,7 +21,8 @@ from . import afx
 
 class Step(NamedTuple):
     """The new tokens of one step: row r's are starts[r] .. starts[r + 1] - 1
-    of m, and belong to sequence seqs[r]. slots, pos and granted are views of
+    of m, and belong to sequence seqs[r]; max_new and max_len are the most of
+    one row and the most tokens of one sequence after them. slots, pos and granted are views of
     the cache's buffers: a step ends with the cache's next call. A row whose
     granted is not its number of tokens was refused (see afx.h): its tokens
     have no slots, and what is computed for them is of no use."""
@@ -34,6 +35,7 @@ class Step(NamedTuple):
     pos: object
     granted: object
     number: int
+    max_len: int
 
 
 class PagedCache:
@@ -98,10 +100,15 @@ class PagedCache:
         self.number += 1
         return torch.cuda.current_stream(self.device).cuda_stream
 
-    def extend(self, seqs, starts, m: int, max_new: int | None = None) -> Step:
+    def extend(self, seqs, starts, m: int, max_new: int | None = None, max_len: int | None = None) -> Step:
         """Sequences grow by the new tokens of their rows: row r's are
-        starts[r] .. starts[r + 1] - 1 of m; max_new (m if not told) is the most
-        of one row."""
+        starts[r] .. starts[r + 1] - 1 of m. max_new (m if not told) is the most
+        of one row, max_len (all that the cache can hold of a sequence if not
+        told) the most tokens of one sequence afterwards. Attention divides its
+        work by them: rows and sequences that have more come out right too, but
+        numbers far from the truth cost time, of single tokens over a long
+        cache most of it. A captured step keeps the numbers that it was
+        captured with: tell the most that its replays will meet."""
         import torch
 
         s, n = self._list(seqs, "seqs"), seqs.numel()
@@ -111,11 +118,15 @@ class PagedCache:
         max_new = m if max_new is None else max_new
         if not 1 <= max_new <= m:
             raise ValueError(f"at most {max_new} of {m} tokens in a row")
+        most = self.max_pages * self.page_tokens
+        max_len = most if max_len is None else max_len
+        if not 1 <= max_len <= most:
+            raise ValueError(f"at most {max_len} tokens of a sequence: the cache holds 1 to {most}")
         with torch.cuda.device(self.device):
             afx.afx_pages_extend_async(self.pages, self.planes, n, s, at, m, self.slots.data_ptr(), self.pos.data_ptr(),
                                        self.granted.data_ptr(), self.ws.data_ptr(), self.ws.numel(), self._stream())
-        return Step(self, seqs, starts, m, max_new, self.slots[:m], self.pos[:m], self.granted[:n],
-                    self.number)
+        return Step(self, seqs, starts, m, max_new, self.slots[:m], self.pos[:m], self.granted[:n], self.number,
+                    max_len)
 
     def fork(self, src, dst):
         """Sequences dst, which hold nothing, become copies of src that share
