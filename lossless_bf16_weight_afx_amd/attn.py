@@ -13,7 +13,8 @@ from the library's entry points:
 It stands before ffn.FeedForward in a layer: r' is that one's r. As there,
 this module only holds buffers and makes calls: everything is enqueued on the
 current stream, which a HIP graph may capture, nothing is allocated after the
-constructor, and one object serves one stream at a time.
+constructor, and the objects over one cache serve one stream at a time: they
+share the memory for the products' outputs and the attention's workspace.
 """
 from __future__ import annotations
 
@@ -77,8 +78,8 @@ class Attention:
         self.xn, self.qn, self.a, self.r_out = new(d), new(nq), new(nq), new(d)
         self.xn_next = new(d) if w_next is not None else None
         # the products' FP32 outputs of a step of m tokens, cleared at once: m rows of q, of k, of v, of b
-        self.y = torch.empty(max_tokens * (nq + 2 * nk + d), dtype=torch.float32, device=dev)
-        self.ws = torch.empty(max(max(self._workspaces()), 16), dtype=torch.uint8, device=dev)
+        self.y = cache.scratch("products", 4 * max_tokens * (nq + 2 * nk + d)).view(torch.float32)
+        self.ws = cache.scratch("attention", max(max(self._workspaces()), 16))
 
     def _attend(self, max_new: int, max_len: int) -> afx.afx_attend:
         return afx.attend(self.q_heads, self.softmax_scale, True, self.window, max_new, max_len)

@@ -71,6 +71,7 @@ class PagedCache:
         self.slots, self.pos, self.granted = new(max_tokens), new(max_tokens), new(max_rows)
         self.map, self.live = new(n_pages), new(1)
         self.number = 0  # calls so far
+        self._scratch = {}
         self.pages = afx.page_table(self.table.data_ptr(), max_pages, self.len.data_ptr(), self.refs.data_ptr(), max_seqs,
                                     max_pages, n_pages, page_tokens)
         self.planes = afx.page_data(self.data.data_ptr(), 2 * per_page, 2 * per_page * n_pages, 2 * layers)
@@ -84,6 +85,17 @@ class PagedCache:
             raise ValueError(f"layer {i} of {self.layers}")
         at = self.data.data_ptr() + 2 * i * self.planes.plane_stride
         return afx.kv_pages(at, at + self.planes.plane_stride, self.n_pages, self.page_tokens, self.kv_heads, self.head_dim)
+
+    def scratch(self, what: str, n: int):
+        """n bytes on the device for what a layer's pass over this cache forms
+        and uses up. Passes follow one another on the cache's stream: those of
+        all layers share them. For constructors: what a larger n replaces stays
+        with those who hold it."""
+        import torch
+
+        if what not in self._scratch or self._scratch[what].numel() < n:
+            self._scratch[what] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return self._scratch[what][:n]
 
     def _list(self, t, what: str, n: int | None = None) -> int:
         import torch
