@@ -84,6 +84,16 @@ class Attention:
     def _attend(self, max_new: int, max_len: int) -> afx.afx_attend:
         return afx.attend(self.q_heads, self.softmax_scale, True, self.window, max_new, max_len)
 
+    def _plan(self, max_new: int, max_len: int, n: int, m: int) -> afx.afx_attend:
+        """The attention of m new tokens of n sequences. Steps of unusual sizes, that the workspace was not made for,
+        are cut into fewer parts, as if their sequences were shorter, or into one, which needs none."""
+        size = lambda p: afx.afx_attend_workspace(p, self.kv, n, m)  # noqa: E731
+        p = self._attend(max_new, max_len)
+        if size(p) > self.ws.numel():
+            shorter = (self._attend(max_new, max_len >> i) for i in range(1, max_len.bit_length()))
+            p = next((s for s in shorter if 0 < size(s) <= self.ws.numel()), self._attend(max_new, 1))
+        return p
+
     def _workspaces(self):
         """The workspaces of single tokens and of drafts of some tokens for every number of rows, and of prompts, over
         sequences of the cache's most tokens and of shorter ones (which may be cut into more parts)."""
@@ -139,9 +149,7 @@ class Attention:
         q, k, v, b = y, y + 4 * m * nq, y + 4 * m * (nq + nk), y + 4 * m * (nq + 2 * nk)
         pos_ptr, pos_ld = (step.pos if pos is None else pos).data_ptr(), pos.stride(0) if self.n_axes > 1 else m
         xn, xn_next = self.xn.data_ptr(), 0 if self.xn_next is None else self.xn_next.data_ptr()
-        p = self._attend(step.max_new, step.max_len)
-        if afx.afx_attend_workspace(p, self.kv, n, m) > self.ws.numel():
-            p = self._attend(step.max_new, 1)  # (a step of unusual sizes: in one part, which needs none)
+        p = self._plan(step.max_new, step.max_len, n, m)
         s = torch.cuda.current_stream(c.device).cuda_stream
         with torch.cuda.device(c.device):
             self.y[:m * (nq + 2 * nk + d)].zero_()

@@ -48,8 +48,8 @@ struct AttendArgs {
     float scale2;
     uint32_t q_and, q_xor;  // what makes q of two of its values
     // Batch rows of at most few_rows query rows a head go to the kernel for few
-    // rows: their tokens are cut into parts of few_part tokens, at most
-    // few_splits. The others' tiles are cut into many_splits equal parts.
+    // rows: their tokens are cut into parts of few_part tokens (more where that
+    // makes more than few_splits). The others' tiles are cut into many_splits equal parts.
     uint32_t few_rows, few_part, few_splits, many_tiles, many_splits;
     // Sums of parts: few: [n_rows][kv_heads][few_rows][few_splits], many: [m][q_heads][many_splits], of d unnormalised
     // outputs, and M and the sum of weights.
@@ -80,16 +80,20 @@ struct BatchRow {
 };
 
 // The positions seen by a batch row that the kernel for few rows takes, from
-// a multiple of its tile on, and the number of parts.
+// a multiple of its tile on, and their parts.
 struct FewRange {
     int32_t base, end;
-    uint32_t splits;
+    uint32_t part, splits;  // tokens of a part (of the last one: the rest), number of parts
     __device__ FewRange(const AttendArgs &a, const BatchRow &row) {
         base = row.begin(a, 0) & ~(int32_t)(kFewTokens - 1);
         end = max(row.end(a, row.n - 1), base);
-        const uint32_t parts = ((uint32_t)(end - base) + a.few_part - 1) / a.few_part;
+        const uint32_t n = (uint32_t)(end - base);
+        part = a.few_part;
+        // (a row longer than was told is cut into as many parts as there is room for, all alike)
+        if (a.few_splits > 1 && n > a.few_splits * a.few_part + kFewTokens)
+            part = ((n + a.few_splits - 1) / a.few_splits + 127) & ~127u;
         // (more rows than there is room for come out of one part)
-        splits = row.n * a.group <= a.few_rows ? min(max(parts, 1u), a.few_splits) : 1;
+        splits = row.n * a.group <= a.few_rows ? min(max((n + part - 1) / part, 1u), a.few_splits) : 1;
     }
 };
 

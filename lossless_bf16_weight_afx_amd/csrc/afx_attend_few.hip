@@ -386,8 +386,8 @@ __global__ __launch_bounds__(kThreads, KC * RG <= 8 ? 2 : 1) void afx_attend_few
     const FewRange range(a, t.row);
     t.splits = range.splits;
     if (t.part >= t.splits) return;
-    t.j0 = range.base + (int32_t)(t.part * a.few_part);
-    t.j1 = t.part + 1 == t.splits ? range.end : t.j0 + (int32_t)a.few_part;
+    t.j0 = range.base + (int32_t)(t.part * range.part);
+    t.j1 = t.part + 1 == t.splits ? range.end : t.j0 + (int32_t)range.part;
     for (uint32_t r0 = 0; r0 < rows; r0 += 16 * RG)
         unit<KC, RG, kFull>(a, t, r0, lds);
 }

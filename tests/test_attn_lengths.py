@@ -45,3 +45,22 @@ def test_lengths_that_are_refused(calls):  # noqa: F811
     c = paged()
     for length in (0, -1, 129):
         refused(calls, c.extend, ints(0), ints(0, 7), 7, 7, length)
+
+
+def test_steps_of_unusual_sizes_are_cut_into_what_there_is_room_for(calls, monkeypatch):  # noqa: F811
+    """Not into one part as soon as the workspace is smaller than the plan's."""
+    c = paged(max_pages=8192, max_tokens=384, max_seqs=40, max_rows=40)
+    t = half(c)
+    for rows, new in ((1, 1), (38, 7), (3, 1)):
+        m = rows * new
+        starts = torch.arange(rows + 1, dtype=torch.int32) * new
+        need = afx.afx_attend_workspace(t._attend(new, 131072), t.kv, rows, m)
+        for part in (1, 2, 3, 8):
+            if need // part < 4 * m * 4 * 66 * 2:
+                continue  # (less than two parts of its queries)
+            monkeypatch.setattr(t, "ws", torch.empty(need // part, dtype=torch.uint8))
+            step = c.extend(torch.arange(rows, dtype=torch.int32), starts, m, new)
+            t.forward(torch.ones(m, 256, dtype=torch.bfloat16), step)
+            p, ws = planned(calls)
+            assert ws == need // part
+            assert ws / 2.5 < afx.afx_attend_workspace(p, t.kv, rows, m) <= ws, (rows, new, part)

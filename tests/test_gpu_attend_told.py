@@ -24,3 +24,15 @@ def test_lengths_that_no_sequence_has(new, max_len):
     b.upload()
     b.run(scale=0.3, max_len=max_len)
     b.check()
+
+
+@pytest.mark.parametrize("new", [1, 4, 60])
+@pytest.mark.parametrize("length, told", [(9000, 520), (9000, 1000), (9000, 4400), (4097, 1030), (1331, 1300), (5003, 5000)])
+@pytest.mark.parametrize("window", [0, 4321])
+def test_sequences_longer_than_was_told(new, length, told, window):
+    """More tokens than the parts that were planned: they are shared out anew, over as many parts."""
+    b = Batch(length + told + new, [length, 300, 1025], [(0, new), (1, min(new, 3)), (2, 1)], kv_heads=1, group=4, page=64,
+              spread=1.5)
+    b.upload()
+    b.run(scale=0.125, max_len=told, window=window)
+    b.check()
