@@ -453,7 +453,8 @@ typedef struct afx_heads {
  * and k_out are BF16 rows; k_out may be NULL when kv is given. With kv, token
  * i's key and value go to slot slots[i]; a slot outside the cache (such as
  * -1) writes none. Slots inside it have to be distinct. Sums and rotations
- * are FP32, angles FP64, and each output is rounded once. Any m (0 does
+ * are FP32 (a value above about 1e19 overflows its head's mean to infinity),
+ * angles FP64, and each output is rounded once. Any m (0 does
  * nothing). Enqueued on stream; returns without waiting. Fastest when rot_dim
  * and the strides are multiples of 8 and the buffers 16-byte aligned. Errors:
  * AFX_E_INVALID_ARG (NULL pointer, nothing to do, a count out of its range,

@@ -171,10 +171,12 @@ Plan plan(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t
         // two workgroups of a CU share its reads: the cheapest number for rows of equal lengths and rows of any
         // (0.55 of the longest, the last part alone) together. Times by tokens of a part, 40 query and 8 key-value
         // heads of 128:
-        //   64 rows of 8192 tokens       1024: 351 us  2048: 332  8192: 316
-        //   64 rows of up to 8192        1024: 191 us  2048: 196  8192: 226
-        //   16 rows of up to 4000         512: 39 us   1024: 40   4096: 59
-        //   1 row of 16000                256: 21 us    512: 20   1024: 24  8192: 111
+        //   64 rows of 8192 tokens       1024: 354 us  2048: 337  8192: 319
+        //   64 rows of up to 8192        1024: 188 us  2048: 192  8192: 226
+        //   16 rows of up to 4000         512: 36 us   1024: 38   4096: 58
+        //   1 row of 16000                256: 20 us    512: 19   1024: 24  8192: 105
+        // The estimate knows no head size. With heads of 64 and 256, what it takes is within 10% of the best of up to
+        // six numbers tried: 1 row of 16000 (13 and 23 us), 16 rows of 4000 (28 and 50), 64 rows of 4096 (48 and 178).
         double best = 1e30;
         for (uint64_t n = 1; n <= kMaxSplits && (n == 1 || tokens > (n / 2) * 256); n *= 2) {
             const uint64_t part = up(up(tokens, n), 128) * 128;
@@ -191,12 +193,15 @@ Plan plan(const afx_attend *p, const afx_kv_pages *kv, uint32_t n_rows, uint32_t
         // 0.022 of its round and 0.012 more as far as every CU has one, its start and end 12, a join 10 and 8 more per
         // 81920 rows of a part. Measured, with 40 query and 8 key-value heads of 128 (tokens over tokens):
         //   parts              1       2       3       4
-        //   2048 over 2048    88 us  125     130     153
-        //   2048 over 4096   205     232     236     249
-        //   2048 over 8192   454     436     422     426
-        //   2048 over 16384  927     809     768     754
-        //   512 over 8192    247     150     117     160
-        //   64 over 16384    475     248     173     134   (16: 59)
+        //   2048 over 2048    79 us  111     112     131
+        //   2048 over 4096   177     198     195     211
+        //   2048 over 8192   413     379     361     375
+        //   2048 over 16384  885     745     698     692
+        //   512 over 8192    232     139     108     149
+        //   64 over 16384    443     235     164     127   (16: 53)
+        // With heads of 64 and 256 what it takes is within 1% of the best of those tried for 2048 over 8192 (131 and 502
+        // us), 512 over 8192 (78 and 150) and 64 over 16384 (38 and 69), and with 20 query and 4 key-value heads of 64
+        // or 128 one part for 2048 over 2048 where three are faster (53 and 71 us, 45 and 64).
         const uint64_t most_splits = std::min<uint64_t>(16, std::max<uint64_t>(1, tokens / 256));
         const double length = (double)tokens - (p->causal ? (double)std::min(most, tokens) / 2 : 0);
         double best = 1e30;

@@ -21,8 +21,11 @@
 // and lose nothing, as their rounding to BF16 is relative.
 //
 // With 40 query and 8 key-value heads of 128: one token of each of 64
-// sequences of up to 8192 tokens takes 191 us, and 5 for the join (1.08 GB of
-// cache, 5.6 TB/s); one token over 131072 81 us (537 MB, 6.6 TB/s), and 5.
+// sequences of up to 8192 tokens takes 189 us, and 5 for the join (1.08 GB of
+// cache, 5.7 TB/s); one token over 131072 80 us (537 MB, 6.7 TB/s), and 5.
+// Heads of 200 to 248 dimensions reload up to 16 values a lane from scratch
+// memory in the loop: 64 x 1 over 4096 tokens of 4 heads of 232 take 225 us,
+// where those of 256, 10% more bytes, take 178.
 #include <type_traits>
 
 #include "afx_attend.h"

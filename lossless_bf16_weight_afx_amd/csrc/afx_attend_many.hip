@@ -23,10 +23,11 @@
 // there, with a tile's time to arrive. A row's running maximum moves only when
 // one of its scores exceeds it by 8 (a factor 2^8), as in afx_attend_few.hip.
 //
-// 2048 tokens over 16384, 40 query and 8 key-value heads of 128: 670-790 us
-// as the clock allows (0.83-0.96 PFLOP/s), and 33 for the join of 4 parts. Of
-// the kernel's cycles the matrix cores work in 40%, vector instructions take
-// 45% to issue and LDS works in 20%: the first two overlap little. 64 rows a
+// 2048 tokens over 16384, 40 query and 8 key-value heads of 128: 660-740 us
+// as the clock allows (0.87-0.97 PFLOP/s), and 30 for the join of 4 parts. Of
+// the kernel's cycles the matrix cores work in 43%, vector instructions take
+// 57% to issue (an exponential 16 cycles, others 4) and LDS works in 22%: the
+// first two hardly overlap. 64 rows a
 // wave, one wave a SIMD, with half the reads of LDS and every exponential
 // between matrix instructions, took as long.
 #include <type_traits>
