@@ -52,6 +52,8 @@ class Attention:
                 raise ValueError(f"a matrix is not one of {shape[0]} x {shape[1]} values")
             if blob.device != dev:
                 raise ValueError("the matrices are on the cache's device")
+            if not blob.is_contiguous() or blob.numel() * blob.element_size() < info.blob_bytes:
+                raise ValueError(f"a blob of {info.blob_bytes} bytes is not whole in {blob.numel() * blob.element_size()}")
         if not 1 <= max_tokens <= cache.max_tokens:
             raise ValueError(f"{max_tokens} tokens: the cache's steps are of 1 to {cache.max_tokens}")
         pairs = 0 if freq is None else freq.numel()

@@ -44,6 +44,8 @@ class FeedForward:
                 raise ValueError(f"a matrix is not one of {shape[0]} x {shape[1]} values")
             if blob.device != w_pre.device:
                 raise ValueError("the matrices and the norm weights are on one device")
+            if not blob.is_contiguous() or blob.numel() * blob.element_size() < info.blob_bytes:
+                raise ValueError(f"a blob of {info.blob_bytes} bytes is not whole in {blob.numel() * blob.element_size()}")
         if max_tokens < 1:
             raise ValueError("max_tokens must be at least 1")
         for t in (w_pre, w_post, block_gate, w_next):
