@@ -18,6 +18,8 @@ share the memory for the products' outputs and the attention's workspace.
 """
 from __future__ import annotations
 
+import math
+
 from . import afx
 from .cache import PagedCache, Step
 
@@ -54,6 +56,8 @@ class Attention:
                 raise ValueError("the matrices are on the cache's device")
             if not blob.is_contiguous() or blob.numel() * blob.element_size() < info.blob_bytes:
                 raise ValueError(f"a blob of {info.blob_bytes} bytes is not whole in {blob.numel() * blob.element_size()}")
+        if d > afx.MAX_NORM_WIDTH or not (0 < eps < math.inf and math.isfinite(scale)):
+            raise ValueError(f"norms of up to {afx.MAX_NORM_WIDTH} values, eps {eps} above 0, scale {scale} finite")
         if not 1 <= max_tokens <= cache.max_tokens:
             raise ValueError(f"{max_tokens} tokens: the cache's steps are of 1 to {cache.max_tokens}")
         pairs = 0 if freq is None else freq.numel()
