@@ -530,10 +530,9 @@ int afx_attend_workspace(const afx_attend *p, const afx_kv_pages *kv, uint32_t n
  * read, and those of out and lse are left as they were. What a query does not
  * see never changes its result, infinities and NaN in it included; an
  * infinite or NaN value that it sees, however little it weighs, makes its
- * output infinite or NaN. Tokens of
- * a page whose id is outside the cache are seen by none, rows whose sequence
- * is outside the table have no tokens, lengths are capped at max_pages pages,
- * and starts at m. Scores and sums are FP32; the weights of the values are
+ * output infinite or NaN. Tokens of a page whose id is outside the cache are
+ * seen by none, rows whose sequence is outside the table have no tokens,
+ * lengths are capped at max_pages pages, and starts at m. Scores and sums are FP32; the weights of the values are
  * rounded to BF16 (the matrix cores' operand), as is out. The same bits on
  * every run. Enqueued on stream; returns without waiting. Errors:
  * AFX_E_INVALID_ARG (NULL pointer, a count out of its range, a table of other

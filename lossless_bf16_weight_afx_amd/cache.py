@@ -22,10 +22,11 @@ from . import afx
 class Step(NamedTuple):
     """The new tokens of one step: row r's are starts[r] .. starts[r + 1] - 1
     of m, and belong to sequence seqs[r]; max_new and max_len are the most of
-    one row and the most tokens of one sequence after them. slots, pos and granted are views of
-    the cache's buffers: a step ends with the cache's next call. A row whose
-    granted is not its number of tokens was refused (see afx.h): its tokens
-    have no slots, and what is computed for them is of no use."""
+    one row and the most tokens of one sequence after them. slots, pos and
+    granted are views of the cache's buffers: a step ends with the cache's
+    next call. A row whose granted is not its number of tokens was refused
+    (see afx.h): its tokens have no slots, and what is computed for them is of
+    no use; the same goes for tokens behind the last row's."""
     cache: "PagedCache"
     seqs: object
     starts: object

@@ -49,7 +49,8 @@ struct AttendArgs {
     uint32_t q_and, q_xor;  // what makes q of two of its values
     // Batch rows of at most few_rows query rows a head go to the kernel for few
     // rows: their tokens are cut into parts of few_part tokens (more where that
-    // makes more than few_splits). The others' tiles are cut into many_splits equal parts.
+    // makes more than few_splits). The others' tiles are cut into many_splits
+    // equal parts.
     uint32_t few_rows, few_part, few_splits, many_tiles, many_splits;
     // Sums of parts: few: [n_rows][kv_heads][few_rows][few_splits], many: [m][q_heads][many_splits], of d unnormalised
     // outputs, and M and the sum of weights.
